@@ -33,9 +33,11 @@ EXPORTS = ("csa2_page_bytes", "csa2_swa_bytes", "csa2_workspace_bytes", "csa2_pr
            "csa2_index", "csa2_attend", "csa2_get_device_error", "csa2_status_string", "csa2_set_profile_events",
            "csa2_launch_count", "csa2_attend_noalloc", "csa2_topk", "csa2_shard_blocks", "csa2_shard_pool",
            "csa2_shard_rescore", "csa2_shard_topk", "csa2_attend_partial", "csa2_combine",
-           "csa2_selftest_wait_timeout")
+           "csa2_selftest_wait_timeout", "csa2_verify", "csa2_plan_tokens", "csa2_norm_rope")
 MAX_SHARDS = 8
 ATTEND_NOALLOC_MAX_ROWS = 512
+MAX_DRAFT, PLAN_MAX_BATCH = 31, 4096
+ROPE_HALVES, ROPE_INVERSE, ROPE_NO_NORM = 1, 2, 4
 KERNEL_BLOCK_SCORE, KERNEL_FLAT_SCORE, KERNEL_POOL_SCORE, KERNEL_SELECT, KERNEL_ATTEND, KERNEL_COMBINE = range(6)
 
 
@@ -82,6 +84,10 @@ def _load():
         "csa2_attend_partial": (C.c_int, [P, I32, P, P, C.c_float, I32, P, P, C.c_uint32, P]),
         "csa2_combine": (C.c_int, [I32, P, P, I32, I32, P, I32, P]),
         "csa2_selftest_wait_timeout": (C.c_int, [P, C.c_uint32, P]),
+        "csa2_verify": (C.c_int, [I32, I32, I32, P, P, P, P, P, P, P, P, P]),
+        "csa2_plan_tokens": (C.c_int, [I32, I32, I32, I32, P, P, P, P, P, P, P, P, P, P, P, P, P]),
+        "csa2_norm_rope": (C.c_int, [I32, I32, I32, P, C.c_int64, P, P, I32, P, C.c_int64, P, P, P, P, P, I32,
+                                     C.c_float, C.c_uint32, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -308,3 +314,92 @@ def csa2_selftest_wait_timeout(error_word, polls: int = 1024, stream=None):
     """Run the bounded-wait self-test: error_word (int32 device tensor of one
     element) receives CSA2_DEV_TIMEOUT once the probe's wait runs out."""
     _check("csa2_selftest_wait_timeout", lib.csa2_selftest_wait_timeout(_ptr(error_word), int(polls), _stream(stream)))
+
+
+# ---------------------------------------------------------------- around the layers
+def _typed(name, t, dtype, shape):
+    """The device pointer of t after its device, type and shape are checked (None passes)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name}: {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError("libcsa2 takes contiguous tensors")
+    return _here(t)
+
+
+def _here(t):
+    if not t.is_cuda:
+        raise ValueError("libcsa2 takes device tensors")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError("libcsa2 takes tensors of the current device")
+    return t.data_ptr()
+
+
+def csa2_verify(target, probs, draft, n_draft, u, n_accepted, tokens, error, stream=None):
+    """Accept drafted tokens draft [batch, k] against target [batch, k+1,
+    vocab] f32 and the drafter's probs [batch, k, vocab] f32 (None: it named
+    its tokens for certain) with random numbers u [batch, k+1]; n_accepted
+    [batch] and tokens [batch, k+1] (kept drafts, drawn token, -1) receive the
+    outcome."""
+    B, k1, V = (int(x) for x in target.shape)
+    f32, i32 = torch.float32, torch.int32
+    _check("csa2_verify", lib.csa2_verify(
+        B, k1 - 1, V, _typed("target", target, f32, (B, k1, V)), _typed("probs", probs, f32, (B, k1 - 1, V)),
+        _typed("draft", draft, i32, (B, k1 - 1)), _typed("n_draft", n_draft, i32, (B,)),
+        _typed("u", u, f32, (B, k1)), _typed("n_accepted", n_accepted, i32, (B,)),
+        _typed("tokens", tokens, i32, (B, k1)), _typed("error", error, i32, (1,)), _stream(stream)))
+
+
+def csa2_plan_tokens(n_tokens, n_new, m, page_table, free_pages, n_free, n_free_out, cu_new, token_req, token_pos,
+                     token_slot, error, stream=None):
+    """Pages and slots of a step's new tokens (int32 tensors throughout):
+    n_tokens, n_new, m [batch]; page_table [batch, max_pages] and free_pages
+    [n_pages] are updated; n_free, n_free_out [1]; cu_new [batch+1];
+    token_req, token_pos, token_slot [max_new]."""
+    B, width = (int(x) for x in page_table.shape)
+    n_pages, room, i32 = int(free_pages.shape[0]), int(token_req.shape[0]), torch.int32
+    _check("csa2_plan_tokens", lib.csa2_plan_tokens(
+        B, width, n_pages, room, _typed("n_tokens", n_tokens, i32, (B,)), _typed("n_new", n_new, i32, (B,)),
+        _typed("m", m, i32, (B,)), _typed("page_table", page_table, i32, (B, width)),
+        _typed("free_pages", free_pages, i32, (n_pages,)), _typed("n_free", n_free, i32, (1,)),
+        _typed("n_free_out", n_free_out, i32, (1,)), _typed("cu_new", cu_new, i32, (B + 1,)),
+        _typed("token_req", token_req, i32, (room,)), _typed("token_pos", token_pos, i32, (room,)),
+        _typed("token_slot", token_slot, i32, (room,)), _typed("error", error, i32, (1,)), _stream(stream)))
+
+
+def _heads(name, t):
+    """(pointer, heads, dim, token stride) of a bf16 [n, heads, dim] tensor whose
+    tokens may lie apart (a slice of a wider projection); None has no heads."""
+    if t is None:
+        return None, 0, 0, 0
+    if t.dtype != torch.bfloat16 or t.dim() != 3:
+        raise ValueError(f"{name}: bfloat16 [n, heads, dim] expected, got {t.dtype} {tuple(t.shape)}")
+    n, h, d = (int(x) for x in t.shape)
+    if t.numel() and (t.stride(2) != 1 or (h > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return _here(t), h, d, t.stride(0) if n > 1 else h * d
+
+
+def csa2_norm_rope(q, k, pos, inv_freq, q_weight, k_weight, eps: float, q_out, k_out, k_out_f32=None, n_valid=None,
+                   flags: int = 0, stream=None):
+    """Normalise (times weight [dim] f32) and rotate the heads of q [n, heads,
+    dim] and k [n, kv_heads, dim] (bf16; either may be None): q_out and k_out
+    bf16, k_out_f32 f32 (one k output may be None).  pos [n] i32; inv_freq
+    [rot_dim / 2] f32 or None; n_valid: device int32 [1] or None; flags:
+    ROPE_HALVES | ROPE_INVERSE | ROPE_NO_NORM."""
+    if q is None and k is None:
+        raise ValueError("csa2_norm_rope needs q or k")
+    qp, h, dq, qs = _heads("q", q)
+    kp, g, dk, ks = _heads("k", k)
+    n, d = int((q if q is not None else k).shape[0]), dq or dk
+    if q is not None and k is not None and (dq != dk or int(k.shape[0]) != n):
+        raise ValueError("q and k differ in tokens or channels")
+    f32, i32, b16 = torch.float32, torch.int32, torch.bfloat16
+    rot = 0 if inv_freq is None else 2 * int(inv_freq.shape[0])
+    _check("csa2_norm_rope", lib.csa2_norm_rope(
+        n, d, h, qp, qs, _typed("q_weight", q_weight, f32, (d,)), _typed("q_out", q_out, b16, (n, h, d)), g, kp, ks,
+        _typed("k_weight", k_weight, f32, (d,)), _typed("k_out", k_out, b16, (n, g, d)),
+        _typed("k_out_f32", k_out_f32, f32, (n, g, d)), _typed("pos", pos, i32, (n,)),
+        _typed("inv_freq", inv_freq, f32, (rot // 2,)), rot, float(eps), int(flags),
+        _typed("n_valid", n_valid, i32, (1,)), _stream(stream)))

@@ -5,6 +5,7 @@
 
 #include "common.cuh"
 #include "index.cuh"
+#include "serve.cuh"
 
 using namespace csa2;
 
@@ -294,6 +295,68 @@ csa2_status csa2_combine(int32_t n_parts, const float *const *o_parts, const flo
         p.lse[i] = lse_parts[i];
     }
     return from_cuda(launch_combine(n_parts, p, batch, heads, out, out_is_fp32, (cudaStream_t)stream));
+}
+
+// ------------------------------------------------------------ around the layers
+csa2_status csa2_verify(int32_t batch, int32_t max_draft, int32_t vocab, const float *target, const float *probs,
+                        const int32_t *draft, const int32_t *n_draft, const float *u, int32_t *n_accepted,
+                        int32_t *tokens, int32_t *error, csa2_stream_t stream)
+{
+    CSA2_TRACE("csa2_verify");
+    if (batch <= 0 || batch > 65535 || max_draft < 0 || max_draft > CSA2_MAX_DRAFT || vocab <= 0 || vocab > 1 << 28)
+        return CSA2_ERR_INVALID_ARG;
+    if (!target || !n_draft || !u || !n_accepted || !tokens || !error || (max_draft > 0 && !draft))
+        return CSA2_ERR_INVALID_ARG;
+    const VerifyArgs a = {batch, max_draft, vocab, target, probs, draft, n_draft, u, n_accepted, tokens, error};
+    return from_cuda(launch_verify(a, (cudaStream_t)stream));
+}
+
+csa2_status csa2_plan_tokens(int32_t batch, int32_t max_pages, int32_t n_pages, int32_t max_new,
+                             const int32_t *n_tokens, const int32_t *n_new, const int32_t *m, int32_t *page_table,
+                             int32_t *free_pages, const int32_t *n_free, int32_t *n_free_out, int32_t *cu_new,
+                             int32_t *token_req, int32_t *token_pos, int32_t *token_slot, int32_t *error,
+                             csa2_stream_t stream)
+{
+    CSA2_TRACE("csa2_plan_tokens");
+    if (batch <= 0 || batch > CSA2_PLAN_MAX_BATCH || max_pages <= 0 || n_pages <= 0 || n_pages >= 1 << 25 ||
+        max_new < 0)
+        return CSA2_ERR_INVALID_ARG;
+    if ((int64_t)max_pages * CSA2_PAGE_ENTRIES > (int64_t)1 << 30) return CSA2_ERR_INVALID_ARG;
+    if (!n_tokens || !n_new || !m || !page_table || !free_pages || !n_free || !n_free_out || !cu_new || !error ||
+        n_free == n_free_out)
+        return CSA2_ERR_INVALID_ARG;
+    if (max_new > 0 && (!token_req || !token_pos || !token_slot)) return CSA2_ERR_INVALID_ARG;
+    const PlanArgs a = {batch, max_pages, n_pages, max_new, n_tokens, n_new, m, page_table, free_pages,
+                        n_free, n_free_out, cu_new, token_req, token_pos, token_slot, error};
+    return from_cuda(launch_plan(a, (cudaStream_t)stream));
+}
+
+csa2_status csa2_norm_rope(int32_t n, int32_t dim, int32_t heads, const uint16_t *q, int64_t q_stride,
+                           const float *q_weight, uint16_t *q_out, int32_t kv_heads, const uint16_t *k,
+                           int64_t k_stride, const float *k_weight, uint16_t *k_out, float *k_out_f32,
+                           const int32_t *pos, const float *inv_freq, int32_t rot_dim, float eps, uint32_t flags,
+                           const int32_t *n_valid, csa2_stream_t stream)
+{
+    CSA2_TRACE("csa2_norm_rope");
+    if (n < 0 || heads < 0 || kv_heads < 0 || heads > 1024 || kv_heads > 1024 || heads + kv_heads == 0)
+        return CSA2_ERR_INVALID_ARG;
+    if (dim != 64 && dim != 128 && dim != 256 && dim != 512) return CSA2_ERR_INVALID_ARG;
+    if (rot_dim != 0 && (rot_dim < 16 || rot_dim > dim || (rot_dim & (rot_dim - 1)))) return CSA2_ERR_INVALID_ARG;
+    if (flags & ~(CSA2_ROPE_HALVES | CSA2_ROPE_INVERSE | CSA2_ROPE_NO_NORM)) return CSA2_ERR_INVALID_ARG;
+    const bool norm = !(flags & CSA2_ROPE_NO_NORM);
+    if (norm && !(eps >= 0.0f)) return CSA2_ERR_INVALID_ARG;
+    if (n == 0) return CSA2_OK;
+    if (rot_dim > 0 && (!pos || !inv_freq)) return CSA2_ERR_INVALID_ARG;
+    if (heads > 0 && (!q || !q_out || (norm && !q_weight) || q_stride < (int64_t)heads * dim || q_stride % 8 ||
+                      !aligned(q, 16) || !aligned(q_out, 16) || !aligned(q_weight, 16)))
+        return CSA2_ERR_INVALID_ARG;
+    if (kv_heads > 0 &&
+        (!k || (!k_out && !k_out_f32) || (norm && !k_weight) || k_stride < (int64_t)kv_heads * dim || k_stride % 8 ||
+         !aligned(k, 16) || !aligned(k_out, 16) || !aligned(k_out_f32, 16) || !aligned(k_weight, 16)))
+        return CSA2_ERR_INVALID_ARG;
+    const NormRopeArgs a = {n, heads, kv_heads, rot_dim, q, k, q_stride, k_stride, q_weight, k_weight, q_out, k_out,
+                            kv_heads > 0 ? k_out_f32 : nullptr, pos, n_valid, inv_freq, eps, flags};
+    return from_cuda(launch_norm_rope(a, dim, (cudaStream_t)stream));
 }
 
 csa2_status csa2_get_device_error(const csa2_cache *cache, int32_t *code_out, csa2_stream_t stream)

@@ -319,6 +319,96 @@ csa2_status csa2_combine(int32_t n_parts, const float *const *o_parts, const flo
                          int32_t batch, int32_t heads, void *out, int32_t out_is_fp32,
                          csa2_stream_t stream);
 
+/* Around the layers ------------------------------------------------------
+ * What a serving program runs beside the CSA2 layers of a step.  The pages
+ * take page tables, queries, latents and token choices as given; these calls
+ * make them.  A step is: csa2_verify settles which drafted tokens stay,
+ * csa2_plan_tokens gives the tokens that come their pages and slots,
+ * csa2_norm_rope prepares queries, latents and indexer keys,
+ * csa2_prefill / csa2_append write them and csa2_index / csa2_attend read
+ * them.  `error` is a device word as in csa2_cache (it may be the cache's).
+ * Rows behind the last token are never written. */
+
+/* Verification of drafted tokens: which drafts stay, and the token after
+ * them, from given random numbers.  Request b has n_draft[b] (0..max_draft)
+ * drafted tokens; draft i is kept if all before it are and
+ *   u[b][i] * q_i(draft[b][i]) < p_i(draft[b][i])
+ * (compared exactly).  With n kept, the next token is drawn from
+ * max(p_n - q_n, 0) if draft n was refused (from p_n where that is zero
+ * everywhere), else from p_n: the first index whose cumulative weight
+ * exceeds u[b][max_draft] times the total, weights of zero, negative and NaN
+ * being never drawn; sums are fp64.
+ *   target [batch][max_draft + 1][vocab] f32: p_i, need not sum to one
+ *   probs  [batch][max_draft][vocab] f32: q_i, or NULL for a drafter that
+ *          names its token without probabilities (q_i = 1 at that token)
+ *   draft [batch][max_draft] i32, n_draft [batch] i32,
+ *   u [batch][max_draft + 1] f32 in [0, 1)
+ *   n_accepted [batch] i32; tokens [batch][max_draft + 1] i32: the kept
+ *          drafts, the drawn token, then -1
+ * max_draft 0..CSA2_MAX_DRAFT.  A drafted token outside the vocabulary is
+ * refused (CSA2_DEV_BAD_INDEX); a row without positive finite weight gives
+ * the last token (CSA2_DEV_BAD_REQUEST). */
+#define CSA2_MAX_DRAFT 31
+csa2_status csa2_verify(int32_t batch, int32_t max_draft, int32_t vocab, const float *target, const float *probs,
+                        const int32_t *draft, const int32_t *n_draft, const float *u, int32_t *n_accepted,
+                        int32_t *tokens, int32_t *error, csa2_stream_t stream);
+
+/* Pages and slots for a step's tokens.  Request b holds n_tokens[b] tokens
+ * (compression m[b], 1 or 2) and gains n_new[b] of them, or drops -n_new[b]
+ * (rejected drafts; all of them when it ends).  It owns the first
+ * ceil((n_tokens / m) / 64) entries of its page_table row.  Pages it no
+ * longer needs are pushed on the stack free_pages[0 .. *n_free), in request
+ * order and ascending within a request; then the pages it comes to need are
+ * taken off the stack's top, in the same order, into its row.  Entries of a
+ * row past the owned pages are neither read nor cleared.  Requests are served
+ * in order: one whose tokens do not fit max_new, or whose pages the stack no
+ * longer holds, gets neither, like every later one that needs some
+ * (CSA2_DEV_CAPACITY); bad lengths or m get nothing (CSA2_DEV_BAD_REQUEST).
+ * n_tokens is not changed: csa2_prefill and csa2_append count tokens in.
+ *   page_table [batch][max_pages], free_pages [n_pages]: updated in place
+ *   n_free, n_free_out: one word each, before and after; not the same word
+ *   cu_new [batch + 1]: prefix sum of the granted tokens
+ *   token_req, token_pos, token_slot [max_new]: of the i-th new token its
+ *          request, its position, and the pool slot (64 * page + row) of the
+ *          entry it completes, -1 if none (an m = 2 pair's first token) or
+ *          if the page id is bad (CSA2_DEV_BAD_PAGE)
+ * Repeating a call before n_tokens, n_new, n_free or the tables' owned parts
+ * change repeats its results.  batch 1..CSA2_PLAN_MAX_BATCH, n_pages < 2^25. */
+#define CSA2_PLAN_MAX_BATCH 4096
+csa2_status csa2_plan_tokens(int32_t batch, int32_t max_pages, int32_t n_pages, int32_t max_new,
+                             const int32_t *n_tokens, const int32_t *n_new, const int32_t *m,
+                             int32_t *page_table, int32_t *free_pages, const int32_t *n_free,
+                             int32_t *n_free_out, int32_t *cu_new, int32_t *token_req, int32_t *token_pos,
+                             int32_t *token_slot, int32_t *error, csa2_stream_t stream);
+
+/* Norm of every query head and latent, with the position rotation.  Per row
+ * x of dim channels (64, 128, 256 or 512):
+ *   y = x / sqrt(mean(x^2) + eps) * weight, then the pairs (a, b) of the
+ *   last rot_dim channels become (a cos t - b sin t, a sin t + b cos t),
+ *   t = pos * inv_freq[i] for pair i (formed in fp64, any position).
+ * rot_dim is 0 or a power of two from 16 to dim; pair i is channels
+ * (2i, 2i + 1) of the range, or (i, i + rot_dim / 2) with CSA2_ROPE_HALVES.
+ * CSA2_ROPE_INVERSE turns by -t (attention outputs: latents serve as values
+ * with their rotation on); CSA2_ROPE_NO_NORM only rotates (weights unused).
+ *   q [n][heads][dim], k [n][kv_heads][dim] bf16 (latents, indexer keys), each
+ *          with its own stride in elements between tokens, a multiple of 8
+ *   q_weight, k_weight f32 [dim]; pos i32 [n]; inv_freq f32 [rot_dim / 2]
+ *   q_out [n][heads][dim], k_out [n][kv_heads][dim] bf16, contiguous (they
+ *          may be the inputs' memory where those are); k_out_f32: the same in
+ *          f32 as csa2_prefill and csa2_append take it; one of the two k
+ *          outputs may be NULL
+ *   n_valid: NULL, or a device word: only the first min(n, *n_valid) tokens
+ *          are read and written (a captured step's padding)
+ * heads or kv_heads may be 0 (its pointers are unused), not both. */
+#define CSA2_ROPE_HALVES  1u
+#define CSA2_ROPE_INVERSE 2u
+#define CSA2_ROPE_NO_NORM 4u
+csa2_status csa2_norm_rope(int32_t n, int32_t dim, int32_t heads, const uint16_t *q, int64_t q_stride,
+                           const float *q_weight, uint16_t *q_out, int32_t kv_heads, const uint16_t *k,
+                           int64_t k_stride, const float *k_weight, uint16_t *k_out, float *k_out_f32,
+                           const int32_t *pos, const float *inv_freq, int32_t rot_dim, float eps, uint32_t flags,
+                           const int32_t *n_valid, csa2_stream_t stream);
+
 /* Attention without a workspace ------------------------------------------
  * The pages have no counterpart to this call; it exists for callers that
  * cannot allocate device memory -- for instance code embedded in a host
