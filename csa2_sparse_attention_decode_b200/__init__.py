@@ -33,7 +33,8 @@ EXPORTS = ("csa2_page_bytes", "csa2_swa_bytes", "csa2_workspace_bytes", "csa2_pr
            "csa2_index", "csa2_attend", "csa2_get_device_error", "csa2_status_string", "csa2_set_profile_events",
            "csa2_launch_count", "csa2_attend_noalloc", "csa2_topk", "csa2_shard_blocks", "csa2_shard_pool",
            "csa2_shard_rescore", "csa2_shard_topk", "csa2_attend_partial", "csa2_combine",
-           "csa2_selftest_wait_timeout", "csa2_verify", "csa2_plan_tokens", "csa2_norm_rope")
+           "csa2_selftest_wait_timeout", "csa2_verify", "csa2_plan_tokens", "csa2_norm_rope",
+           "csa2_prompt_attend", "csa2_prompt_workspace_bytes")
 MAX_SHARDS = 8
 ATTEND_NOALLOC_MAX_ROWS = 512
 MAX_DRAFT, PLAN_MAX_BATCH = 31, 4096
@@ -88,6 +89,9 @@ def _load():
         "csa2_plan_tokens": (C.c_int, [I32, I32, I32, I32, P, P, P, P, P, P, P, P, P, P, P, P, P]),
         "csa2_norm_rope": (C.c_int, [I32, I32, I32, P, C.c_int64, P, P, I32, P, C.c_int64, P, P, P, P, P, I32,
                                      C.c_float, C.c_uint32, P, P]),
+        "csa2_prompt_workspace_bytes": (SZ, [I32, I32, I32]),
+        "csa2_prompt_attend": (C.c_int, [I32, P, P, I32, I32, I32, P, P, C.c_int64, I32, C.c_float, P, I32, P, P, P,
+                                         SZ, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -403,3 +407,27 @@ def csa2_norm_rope(q, k, pos, inv_freq, q_weight, k_weight, eps: float, q_out, k
         _typed("k_out_f32", k_out_f32, f32, (n, g, d)), _typed("pos", pos, i32, (n,)),
         _typed("inv_freq", inv_freq, f32, (rot // 2,)), rot, float(eps), int(flags),
         _typed("n_valid", n_valid, i32, (1,)), _stream(stream)))
+
+
+def csa2_prompt_workspace_bytes(n_q: int, heads: int, n_k: int) -> int:
+    return int(lib.csa2_prompt_workspace_bytes(n_q, heads, n_k))
+
+
+def csa2_prompt_attend(q, lat, cu_q, cu_k, window: int, scale: float, out, lse, error, ws, stream=None):
+    """Causal attention of packed prompts q [n_q, heads, 512] over latents lat
+    [n_k, 512] (bf16; rows may lie apart), request b holding tokens
+    cu_q[b]..cu_q[b+1] and latents cu_k[b]..cu_k[b+1]; window 0 sees
+    everything.  out like q, bf16 or f32; lse [n_q, heads] f32 or None; ws:
+    uint8, csa2_prompt_workspace_bytes(n_q, heads, n_k)."""
+    n_q, heads = int(q.shape[0]), int(q.shape[1])
+    i32, b16 = torch.int32, torch.bfloat16
+    if lat.dtype != b16 or lat.dim() != 2 or lat.shape[1] != LATENT or (lat.numel() and lat.stride(1) != 1):
+        raise ValueError(f"lat: rows of {LATENT} bfloat16 expected, got {lat.dtype} {tuple(lat.shape)}")
+    n_k, batch = int(lat.shape[0]), int(cu_q.shape[0]) - 1
+    fp32 = out.dtype == torch.float32
+    _check("csa2_prompt_attend", lib.csa2_prompt_attend(
+        batch, _typed("cu_q", cu_q, i32, (batch + 1,)), _typed("cu_k", cu_k, i32, (batch + 1,)), n_q, n_k, heads,
+        _typed("q", q, b16, (n_q, heads, LATENT)), _here(lat), lat.stride(0) if n_k > 1 else LATENT, int(window),
+        float(scale), _typed("out", out, torch.float32 if fp32 else b16, (n_q, heads, LATENT)), int(fp32),
+        _typed("lse", lse, torch.float32, (n_q, heads)), _typed("error", error, i32, (1,)),
+        _typed("ws", ws, torch.uint8, (ws.numel(),)), ws.numel(), _stream(stream)))

@@ -359,6 +359,32 @@ csa2_status csa2_norm_rope(int32_t n, int32_t dim, int32_t heads, const uint16_t
     return from_cuda(launch_norm_rope(a, dim, (cudaStream_t)stream));
 }
 
+size_t csa2_prompt_workspace_bytes(int32_t n_q, int32_t heads, int32_t n_k)
+{
+    if (n_q <= 0 || heads <= 0 || heads > 128 || n_k < 0) return 0;
+    return prompt_workspace_bytes(n_q, heads, n_k);
+}
+
+csa2_status csa2_prompt_attend(int32_t batch, const int32_t *cu_q, const int32_t *cu_k, int32_t n_q, int32_t n_k,
+                               int32_t heads, const uint16_t *q, const uint16_t *lat, int64_t lat_stride,
+                               int32_t window, float scale, void *out, int32_t out_is_fp32, float *lse,
+                               int32_t *error, void *ws, size_t ws_bytes, csa2_stream_t stream)
+{
+    CSA2_TRACE("csa2_prompt_attend");
+    if (batch <= 0 || n_q < 0 || n_k < 0 || heads <= 0 || heads > 128 || window < 0) return CSA2_ERR_INVALID_ARG;
+    if ((int64_t)n_q * heads > INT32_MAX - 64 || n_k > INT32_MAX - 128) return CSA2_ERR_INVALID_ARG;
+    if (!cu_q || !cu_k || !error) return CSA2_ERR_INVALID_ARG;
+    if (n_q == 0) return CSA2_OK;
+    if (!q || !out || !ws || !aligned(q, 16) || !aligned(out, 16) || !aligned(ws, 256)) return CSA2_ERR_INVALID_ARG;
+    if (n_k > 0 && (!lat || !aligned(lat, 16) || lat_stride < CSA2_LATENT || lat_stride % 8 ||
+                    lat_stride >= (int64_t)1 << 38))
+        return CSA2_ERR_INVALID_ARG;
+    if (ws_bytes < prompt_workspace_bytes(n_q, heads, n_k)) return CSA2_ERR_INVALID_ARG;
+    const PromptArgs a = {batch, cu_q, cu_k, n_q, n_k, heads, q, lat, lat_stride, window, scale, out, out_is_fp32, lse,
+                          error, ws};
+    return from_cuda(launch_prompt_attend(a, (cudaStream_t)stream));
+}
+
 csa2_status csa2_get_device_error(const csa2_cache *cache, int32_t *code_out, csa2_stream_t stream)
 {
     CSA2_TRACE("csa2_get_device_error");

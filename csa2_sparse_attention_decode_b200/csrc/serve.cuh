@@ -44,4 +44,21 @@ struct VerifyArgs {
 };
 cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t st);
 
+struct PromptArgs {
+    int32_t batch;
+    const int32_t *cu_q, *cu_k;
+    int32_t n_q, n_k, heads;
+    const uint16_t *q, *lat;
+    int64_t lat_stride;                        // elements from latent to latent
+    int32_t window;
+    float scale;
+    void *out;
+    int32_t out_is_fp32;
+    float *lse;
+    int32_t *error;
+    void *ws;
+};
+size_t prompt_workspace_bytes(int64_t n_q, int heads, int64_t n_k);
+cudaError_t launch_prompt_attend(const PromptArgs &a, cudaStream_t st);
+
 }  // namespace csa2

@@ -325,8 +325,8 @@ csa2_status csa2_combine(int32_t n_parts, const float *const *o_parts, const flo
  * make them.  A step is: csa2_verify settles which drafted tokens stay,
  * csa2_plan_tokens gives the tokens that come their pages and slots,
  * csa2_norm_rope prepares queries, latents and indexer keys,
- * csa2_prefill / csa2_append write them and csa2_index / csa2_attend read
- * them.  `error` is a device word as in csa2_cache (it may be the cache's).
+ * csa2_prompt_attend attends a prompt's tokens, csa2_prefill / csa2_append
+ * write them and csa2_index / csa2_attend read them.  `error` is a device word as in csa2_cache (it may be the cache's).
  * Rows behind the last token are never written. */
 
 /* Verification of drafted tokens: which drafts stay, and the token after
@@ -408,6 +408,36 @@ csa2_status csa2_norm_rope(int32_t n, int32_t dim, int32_t heads, const uint16_t
                            int64_t k_stride, const float *k_weight, uint16_t *k_out, float *k_out_f32,
                            const int32_t *pos, const float *inv_freq, int32_t rot_dim, float eps, uint32_t flags,
                            const int32_t *n_valid, csa2_stream_t stream);
+
+/* Attention of packed prompts over the raw latents ([daiw] factor table: one
+ * 512-dim latent shared by all heads, used as both K and V).  Request b's
+ * queries are tokens [cu_q[b], cu_q[b+1]) of q, its latents rows
+ * [cu_k[b], cu_k[b+1]) of lat; its queries are the last of its latents, so a
+ * prompt that continues brings the latents it still sees.  Query i of n over
+ * n_k latents sees latents j <= n_k - n + i, with window > 0 the last
+ * `window` of them:
+ *   o = sum_j softmax_j(scale * q . lat_j) lat_j
+ * It is what a layer that sees its window alone computes for a prompt
+ * (window = CSA2_SWA), and a whole layer while every entry is selected
+ * (window = 0); with n = 1 it is a decode step over raw latents.
+ *   cu_q, cu_k [batch + 1] i32, from 0, non-decreasing; q [n_q][heads][512]
+ *          bf16; lat [n_k] rows of 512 bf16, lat_stride elements apart (a
+ *          multiple of 8)
+ *   out [n_q][heads][512] bf16, or f32 (out_is_fp32 = 1, with the softmax
+ *          weights kept to 16 bits); a query without keys gets zeros
+ *   lse [n_q][heads] f32 or NULL: ln sum_j exp(scale * q . lat_j), -inf
+ *          without keys; with f32 outputs what csa2_combine takes
+ *   ws: at least csa2_prompt_workspace_bytes(), 256-byte aligned; its
+ *          contents are not kept.  Calls that may overlap need one each.
+ * Tokens from cu_q[batch] on are left as they were.  A latent that is not
+ * finite turns the queries that see it to NaN and no other.  cu_q or cu_k
+ * that fall or pass n_q or n_k set CSA2_DEV_BAD_REQUEST; nothing outside the
+ * given arrays is read or written.  heads 1..128, n_q * heads < 2^31 - 64. */
+size_t csa2_prompt_workspace_bytes(int32_t n_q, int32_t heads, int32_t n_k);
+csa2_status csa2_prompt_attend(int32_t batch, const int32_t *cu_q, const int32_t *cu_k, int32_t n_q, int32_t n_k,
+                               int32_t heads, const uint16_t *q, const uint16_t *lat, int64_t lat_stride,
+                               int32_t window, float scale, void *out, int32_t out_is_fp32, float *lse,
+                               int32_t *error, void *ws, size_t ws_bytes, csa2_stream_t stream);
 
 /* Attention without a workspace ------------------------------------------
  * The pages have no counterpart to this call; it exists for callers that
