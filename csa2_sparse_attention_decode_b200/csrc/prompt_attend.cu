@@ -44,11 +44,12 @@ namespace {
 constexpr int D = CSA2_LATENT;
 constexpr int KT = 128;                        // keys per tile
 constexpr int RT = 64;                         // rows per tile
-constexpr int SOFT_WARPS = 8;
-constexpr int THREADS = (SOFT_WARPS + 2) * 32;
+constexpr int SOFT_WARPS = 8, STORE_WARPS = 4;   // then the producer's warp and the MMAs'
+constexpr int LOAD_WARP = SOFT_WARPS + STORE_WARPS, MMA_WARP = LOAD_WARP + 1;
+constexpr int THREADS = (MMA_WARP + 1) * 32;
 constexpr int K_SLAB = KT * 128;               // 64 channels of the keys: 16 KB
 constexpr int Q_SLAB = RT * 128;               // 8 KB
-constexpr int P_BYTES = KT * 128;              // [key][row] bf16, 16 KB
+constexpr int P_BYTES = KT * 128;              // [key][row] bf16, 16 KB; twice, for P's low parts or the output's staging
 constexpr int CHUNKS = 4;                      // of 128 channels
 constexpr int K_OFF = 0, Q_OFF = 8 * K_SLAB, P_OFF = Q_OFF + 8 * Q_SLAB;
 constexpr uint32_t TMEM_COLS = 512;
@@ -56,28 +57,31 @@ constexpr uint32_t S_COL = 256, O_COL = 0;
 constexpr uint32_t IDESC_S = idesc_f16(KT, RT, true, false, false);
 constexpr uint32_t IDESC_O = idesc_f16(128, RT, true, true, true);
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
-constexpr float RISE = 8.0f;                   // how far (in log2) a score may pass the reference
+constexpr float RISE = 32.0f;                  // how far (in log2) a score may pass the reference
+constexpr float FRESH = -3.0e38f;              // reference of a row that has seen no key: every score passes it
+constexpr int CTAS = 148;                      // one per SM
 constexpr int MAX_SPLIT_TILES = 2 * THREADS;   // row tiles that the split path plans in every CTA
 
 struct Segment {                               // n consecutive key tiles of one row tile
     int tile, n, key0;                         // key0: first key of the first of them
     int max_lo, min_hi;                        // keys in [max_lo, min_hi) are seen by every live row
     int slot;                                  // partial result's slot, -1: the segment is the whole row tile
+    bool uniform;                              // every row sees [max_lo, min_hi), which is not empty
+    bool boxed;                                // every row that exists belongs to a request
 };
 
 struct Misc {
-    uint64_t q_full, q_empty, k_full[CHUNKS], k_empty[CHUNKS], s_full, p_full, o_full, seg_full[2], seg_empty[2], drain;
+    uint64_t q_full, q_empty, k_full[CHUNKS], k_empty[CHUNKS], s_full, p_full, o_full, o_empty, fac_full[2], seg_full[2], seg_empty[2], drain;
     Segment seg[2];
     int lo[2][RT], hi[2][RT];
-    float muse[RT], lim[RT], fac[RT];
+    alignas(16) float muse[RT], red[4][RT], fac[2][RT];
     uint32_t tmem;
     int abort;
-    int64_t first_unit, n_units;               // split path: this CTA's share
+    int64_t n_units;                           // split path: this CTA's share
     int first_tile, first_at;
-    int scan[THREADS / 32];
 };
-constexpr size_t smem_bytes(bool split_p) { return P_OFF + (split_p ? 2 : 1) * P_BYTES + sizeof(Misc); }
-static_assert(smem_bytes(true) <= 232448, "shared memory of one CTA");
+constexpr size_t SMEM_BYTES = P_OFF + 2 * P_BYTES + sizeof(Misc);
+static_assert(SMEM_BYTES <= 232448, "shared memory of one CTA");
 
 struct Args {
     const int32_t *cu_q, *cu_k;
@@ -109,11 +113,10 @@ __device__ __forceinline__ int request_of(const Args &a, int t)
 // the prefix sums look, non-decreasing in t where they are sound.
 __device__ __forceinline__ void key_range(const Args &a, int b, int t, int &lo, int &hi)
 {
-    const int64_t q1 = __ldg(a.cu_q + b + 1);
-    const int64_t k0 = max(0, min(a.n_k, __ldg(a.cu_k + b))), k1 = max(0, min(a.n_k, __ldg(a.cu_k + b + 1)));
-    const int64_t end = max(k0, min(k1, k1 - (q1 - t) + 1));
-    hi = (int)end;
-    lo = (int)(a.window > 0 ? max(k0, end - a.window) : k0);
+    const int back = max(1, min(a.n_q, __ldg(a.cu_q + b + 1)) - t);    // this token and those behind it
+    const int k0 = max(0, min(a.n_k, __ldg(a.cu_k + b))), k1 = max(0, min(a.n_k, __ldg(a.cu_k + b + 1)));
+    hi = max(k0, k1 - back + 1);
+    lo = a.window > 0 ? max(k0, hi - a.window) : k0;
 }
 
 // Key tiles of a row tile, 0 if it has no live row; key0 gets the first key
@@ -121,10 +124,10 @@ __device__ __forceinline__ void key_range(const Args &a, int b, int t, int &lo, 
 // the walk goes request by request and skips what lies between.
 __device__ __forceinline__ int key_tiles(const Args &a, int live, int tile, int which, int &key0)
 {
-    int t = (int)((int64_t)tile * RT / a.heads);
+    int t = tile * RT / a.heads;
     key0 = 0;
     if (t >= live) return 0;
-    const int t1 = (int)min((int64_t)live - 1, ((int64_t)tile * RT + RT - 1) / a.heads);
+    const int t1 = min(live - 1, (tile * RT + RT - 1) / a.heads);
     int n = 0, p = 0;
     for (int b = request_of(a, t); t <= t1; ++b) {
         if (b < a.batch - 1 && __ldg(a.cu_q + b + 1) <= t) continue;   // an empty request
@@ -144,12 +147,16 @@ __device__ __forceinline__ int key_tiles(const Args &a, int live, int tile, int 
     return max(1, n);                                                  // rows without keys are written too
 }
 
-// The next key tile: behind this one, or where the first row with keys left begins.
-__device__ __forceinline__ int next_tile(const int *lo, const int *hi, int key0, int &row)
+// The next key tile: behind this one, or where the first row with keys left
+// begins.  A whole warp calls it; lo and hi are non-decreasing over the rows.
+__device__ __forceinline__ int next_tile(const Segment &g, const int *lo, const int *hi, int key0)
 {
     key0 += KT;
-    while (row < RT && hi[row] <= key0) ++row;
-    return row < RT ? max(key0, lo[row]) : key0;
+    if (g.uniform || key0 < g.min_hi) return key0;
+    const int lane = threadIdx.x & 31;
+    const uint32_t a = __ballot_sync(~0u, hi[lane] > key0), b = __ballot_sync(~0u, hi[32 + lane] > key0);
+    const int row = a ? __ffs(a) - 1 : b ? 31 + __ffs(b) : -1;
+    return row < 0 ? key0 : max(key0, lo[row]);
 }
 
 __device__ __forceinline__ float ex2(float x)
@@ -175,6 +182,14 @@ __device__ __forceinline__ bool warp_wait(Misc *m, uint64_t *bar, uint32_t parit
     return __all_sync(~0u, wait(m, bar, parity));
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.b32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
+}
+
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(SOFT_WARPS * 32) : "memory"); }
 __device__ __forceinline__ bool soft_any(bool v)
 {
@@ -185,6 +200,29 @@ __device__ __forceinline__ bool soft_any(bool v)
                  : "memory");
     return r != 0;
 }
+
+// The two warps that fill a box of the output.
+__device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %0, 64;" ::"r"(2 + group) : "memory"); }
+__device__ __forceinline__ bool group_any(int group, bool v)
+{
+    uint32_t r;
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.b32 p, %1, 0;\nbar.red.or.pred q, %2, 64, p;\nselp.b32 %0, 1, 0, q;\n}\n"
+                 : "=r"(r)
+                 : "r"((uint32_t)v), "r"(2 + group)
+                 : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];\n\t"
+                 "cp.async.bulk.commit_group;" ::"l"((uint64_t)map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(src))
+                 : "memory");
+}
+// All but the thread's N newest bulk stores have read their boxes.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Column sums or maxima of a warp's 32 x 32 values (one row per lane): lane c gets column c's.
 template <bool MAX>
@@ -215,7 +253,7 @@ __device__ void producer(const Args &a, Misc *m, uint8_t *sm, const CUtensorMap 
     int64_t left = SPLIT ? m->n_units : 0;
     uint32_t unit = 0, s = 0;
     for (;; ++s) {
-        Segment g = {-1, 0, 0, 0, 0, -1};
+        Segment g = {-1, 0, 0, 0, 0, -1, false, false};
         if (SPLIT) {
             for (; left > 0 && tile < a.tiles; ++tile, at = 0) {
                 const int total = key_tiles(a, live, tile, at, g.key0);
@@ -238,26 +276,34 @@ __device__ void producer(const Args &a, Misc *m, uint8_t *sm, const CUtensorMap 
                 break;
             }
         }
-        const uint32_t r = s & 1;
-        bool ok = warp_wait(m, &m->seg_empty[r], ((s >> 1) & 1) ^ 1);
-        if (ok && g.tile >= 0) {
-            int max_lo = 0, min_hi = INT32_MAX;
+        int lo[2] = {0, 0}, hi[2] = {-1, -1};                          // hi < 0: no such row
+        if (g.tile >= 0) {
+            int max_lo = 0, min_hi = INT32_MAX, min_lo = INT32_MAX, max_hi = -1;
 #pragma unroll
-            for (int i = lane; i < RT; i += 32) {
-                const int64_t row = (int64_t)g.tile * RT + i;
-                const int t = (int)min(row / a.heads, (int64_t)INT32_MAX);
-                int lo = 0, hi = -1;                                   // hi < 0: no such row
+            for (int i = 0; i < 2; ++i) {
+                const int t = (g.tile * RT + 32 * i + lane) / a.heads;
                 if (t < live) {
-                    key_range(a, request_of(a, t), t, lo, hi);
-                    if (hi <= lo) lo = hi = 0;                         // no keys
-                    max_lo = max(max_lo, lo);
-                    min_hi = min(min_hi, hi);
+                    key_range(a, request_of(a, t), t, lo[i], hi[i]);
+                    if (hi[i] <= lo[i]) lo[i] = hi[i] = 0;             // no keys
+                    max_lo = max(max_lo, lo[i]);
+                    min_hi = min(min_hi, hi[i]);
+                    min_lo = min(min_lo, lo[i]);
+                    max_hi = max(max_hi, hi[i]);
                 }
-                m->lo[r][i] = lo;
-                m->hi[r][i] = hi;
             }
             g.max_lo = __reduce_max_sync(~0u, max_lo);
             g.min_hi = __reduce_min_sync(~0u, min_hi);
+            g.uniform = __reduce_min_sync(~0u, min_lo) == g.max_lo && __reduce_max_sync(~0u, max_hi) == g.min_hi && g.min_hi > 0;
+            g.boxed = (int64_t)live * a.heads >= min((int64_t)(g.tile + 1) * RT, (int64_t)a.n_q * a.heads);
+        }
+        const uint32_t r = s & 1;
+        bool ok = warp_wait(m, &m->seg_empty[r], ((s >> 1) & 1) ^ 1);
+        if (ok) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                m->lo[r][32 * i + lane] = lo[i];
+                m->hi[r][32 * i + lane] = hi[i];
+            }
         }
         if (ok && lane == 0) m->seg[r] = g;
         __syncwarp();
@@ -267,17 +313,17 @@ __device__ void producer(const Args &a, Misc *m, uint8_t *sm, const CUtensorMap 
         ok = ok && warp_wait(m, &m->q_empty, (s & 1) ^ 1);
         if (ok && lane == 0) {
             mbar_arrive_expect_tx(&m->q_full, 8 * Q_SLAB);
-            for (int i = 0; i < 8; ++i) tma_load_2d(sm + Q_OFF + i * Q_SLAB, map_q, 64 * i, g.tile * RT, &m->q_full);
+            tma_load_3d(sm + Q_OFF, map_q, 0, g.tile * RT, 0, &m->q_full);
         }
-        int key0 = g.key0, row = 0;
-        for (int k = 0; ok && k < g.n; ++k, ++unit, key0 = next_tile(m->lo[r], m->hi[r], key0, row)) {
+        int key0 = g.key0;
+        for (int k = 0; ok && k < g.n; ++k, ++unit, key0 = next_tile(g, m->lo[r], m->hi[r], key0)) {
+#pragma unroll 1
             for (int c = 0; c < CHUNKS; ++c) {
                 ok = warp_wait(m, &m->k_empty[c], (unit & 1) ^ 1);
                 if (!ok) break;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&m->k_full[c], 2 * K_SLAB);
-                    for (int i = 2 * c; i < 2 * c + 2; ++i)
-                        tma_load_2d(sm + K_OFF + i * K_SLAB, map_k, 64 * i, key0, &m->k_full[c]);
+                    tma_load_3d(sm + K_OFF + 2 * c * K_SLAB, map_k, 0, key0, 2 * c, &m->k_full[c]);
                 }
             }
         }
@@ -294,7 +340,10 @@ __device__ void producer(const Args &a, Misc *m, uint8_t *sm, const CUtensorMap 
 template <bool SPLIT_P>
 __device__ void mma_issuer(Misc *m, uint8_t *sm)
 {
-    const uint32_t ka = smem_addr(sm + K_OFF), qa = smem_addr(sm + Q_OFF), pa = smem_addr(sm + P_OFF), tb = m->tmem;
+    // Descriptors of the operands' first steps; a step on adds its bytes / 16.
+    const uint64_t k_keys = smem_desc(smem_addr(sm + K_OFF), 16, 1024), q_rows = smem_desc(smem_addr(sm + Q_OFF), 16, 1024);
+    const uint64_t k_chans = smem_desc(smem_addr(sm + K_OFF), K_SLAB, 1024), p_rows = smem_desc(smem_addr(sm + P_OFF), 8192, 1024);
+    const uint32_t tb = m->tmem;
     uint32_t unit = 0;
     for (uint32_t s = 0;; ++s) {
         const uint32_t r = s & 1;
@@ -304,27 +353,25 @@ __device__ void mma_issuer(Misc *m, uint8_t *sm)
         if (n == 0) return;
         if (!wait(m, &m->q_full, s & 1)) return;
         for (int k = 0; k < n; ++k, ++unit) {
+#pragma unroll
             for (int c = 0; c < CHUNKS; ++c) {
                 if (!wait(m, &m->k_full[c], unit & 1)) return;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int kk = 8 * c + i;
-                    mma_ss(tb + S_COL, smem_desc(ka + (kk >> 2) * K_SLAB + (kk & 3) * 32, 16, 1024),
-                           smem_desc(qa + (kk >> 2) * Q_SLAB + (kk & 3) * 32, 16, 1024), IDESC_S, kk > 0 ? 1u : 0u);
-                }
+                for (int i = 0; i < 8; ++i)
+                    mma_ss(tb + S_COL, k_keys + ((2 * c + (i >> 2)) * K_SLAB + (i & 3) * 32) / 16,
+                           q_rows + ((2 * c + (i >> 2)) * Q_SLAB + (i & 3) * 32) / 16, IDESC_S, (c > 0 || i > 0) ? 1u : 0u);
             }
             mma_commit(&m->s_full);
             if (k == n - 1) mma_commit(&m->q_empty);
             if (!wait(m, &m->p_full, unit & 1)) return;
+            if (k == 0 && !wait(m, &m->o_empty, (s & 1) ^ 1)) return;  // the last row tile's output is out of O
             fence_after_sync();
+#pragma unroll
             for (int c = 0; c < CHUNKS; ++c) {
 #pragma unroll
-                for (int part = 0; part < (SPLIT_P ? 2 : 1); ++part)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        mma_ss(tb + O_COL + RT * c, smem_desc(ka + 2 * c * K_SLAB + i * 2048, K_SLAB, 1024),
-                               smem_desc(pa + part * P_BYTES + i * 2048, 8192, 1024), IDESC_O,
-                               (k > 0 || part > 0 || i > 0) ? 1u : 0u);
+                for (int i = 0; i < (SPLIT_P ? 16 : 8); ++i)
+                    mma_ss(tb + O_COL + RT * c, k_chans + (2 * c * K_SLAB + (i & 7) * 2048) / 16,
+                           p_rows + ((i >> 3) * P_BYTES + (i & 7) * 2048) / 16, IDESC_O, (k > 0 || i > 0) ? 1u : 0u);
                 mma_commit(&m->k_empty[c]);
             }
             if (k == n - 1) mma_commit(&m->o_full);
@@ -338,34 +385,142 @@ __device__ __forceinline__ uint32_t pack2(float a, float b)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// Channel d, row q of a part lies at part_at(q, d): four rows side by side, so
+// that a warp (32 channels) stores 512 bytes at once.
+__device__ __forceinline__ size_t part_at(int q, int d)
+{
+    return ((size_t)((d >> 7) * (RT / 4) + (q >> 2)) * 128 + (d & 127)) * 4 + (q & 3);
+}
+
+// 16 lanes x 32 columns: lane t gets, of each 8 columns, columns 2 (t % 4) and
+// the next, in rows t / 4 (two registers) and t / 4 + 8 (two more).
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : CSA2_R8(0), CSA2_R8(8)
+                 : "r"(taddr));
+}
+
+// The output of a row tile, by four warps of their own: warp w takes channels
+// 32 w .. 32 w + 31 of every chunk while the others are at the next row tile.
+//
+// bf16: O is turned round with stmatrix into boxes of 64 channels x 32 rows,
+// which two warps fill and a bulk store takes away; four such boxes are in
+// turn.  (Element stores of the same lines, shuffled or staged, took 5500
+// cycles a row tile: the next S leaves the shared-memory pipe little time.)
+// f32: a warp's 32 channels are a line, stored as they are.
+// A part keeps f32 sums, four rows side by side.
+template <bool SPLIT_P>
+__device__ void store(const Args &a, Misc *m, uint8_t *stage, const CUtensorMap *map_out)
+{
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3, mate = w & 1, group = w >> 1;
+    const bool storer = lane == 0 && mate == 0;
+    const uint32_t tb = m->tmem + ((uint32_t)(32 * w) << 16) + O_COL;
+    // matrix lane / 8 of a stmatrix: 8 channels, x the 8 rows whose addresses the lanes give
+    const int put = (lane & 7) * 128 + (((4 * mate + (lane >> 3)) ^ (lane & 7)) << 4);
+    for (uint32_t s = 0;; ++s) {
+        const uint32_t r = s & 1;
+        if (group_any(group, !wait(m, &m->seg_full[r], (s >> 1) & 1))) break;          // both warps leave, or none
+        const int tile = m->seg[r].tile, slot = m->seg[r].slot;
+        const bool boxed = m->seg[r].boxed;
+        const uint32_t live[2] = {__ballot_sync(~0u, m->hi[r][lane] >= 0), __ballot_sync(~0u, m->hi[r][32 + lane] >= 0)};
+        if (lane == 0) mbar_arrive(&m->seg_empty[r]);
+        if (tile < 0) break;
+        wait(m, &m->fac_full[r], (s >> 1) & 1);
+        wait(m, &m->o_full, s & 1);
+        fence_after_sync();
+        const int64_t row0 = (int64_t)tile * RT;
+        const float *fac = m->fac[r];
+        if (slot >= 0 || SPLIT_P) {
+#pragma unroll 1
+            for (int ch = 0; ch < 2 * CHUNKS; ++ch) {
+                const int c = ch >> 1, half = ch & 1, d = 128 * c + 32 * w + lane;
+                uint32_t o[32];
+                tmem_ld32(tb + RT * c + 32 * half, o);
+                tmem_ld_wait();
+                if (slot >= 0) {
+                    float *part = a.part_o + (size_t)slot * RT * D;
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4)
+                        *reinterpret_cast<uint4 *>(part + part_at(32 * half + j, d)) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                } else {
+                    float *out = (float *)a.out + (size_t)(row0 + 32 * half) * D + d;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (live[half] >> j & 1) out[(size_t)j * D] = __uint_as_float(o[j]) * fac[32 * half + j];
+                }
+            }
+        } else {
+#pragma unroll 1
+            for (int ch = 0; ch < 2 * CHUNKS; ++ch) {
+                const int c = ch >> 1, half = ch & 1;
+                uint32_t lo[16], hi[16];                               // channels 0-15 and 16-31 of the warp's
+                tmem_ld_16x32(tb + RT * c + 32 * half, lo);
+                tmem_ld_16x32(tb + (16u << 16) + RT * c + 32 * half, hi);
+                tmem_ld_wait();
+                uint8_t *box = stage + (2 * group + half) * (32 * 128);
+                if (storer) bulk_wait_read<1>();                       // all but the newest store have read their box
+                group_sync(group);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {                          // rows 8i .. 8i+7
+                    const float2 f = *reinterpret_cast<const float2 *>(fac + 32 * half + 8 * i + 2 * (lane & 3));
+                    uint32_t v[4];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        v[k] = pack2(__uint_as_float(lo[4 * i + 2 * k]) * f.x, __uint_as_float(lo[4 * i + 2 * k + 1]) * f.y);
+                        v[2 + k] = pack2(__uint_as_float(hi[4 * i + 2 * k]) * f.x, __uint_as_float(hi[4 * i + 2 * k + 1]) * f.y);
+                    }
+                    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     smem_addr(box + put) + 1024 * i),
+                                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                                 : "memory");
+                }
+                fence_proxy_async_smem();
+                group_sync(group);
+                if (boxed) {
+                    if (storer) tma_store_3d(map_out, box, 0, tile * RT + 32 * half, 2 * c + group);
+                } else {                                               // some rows belong to no request
+                    for (int q = 16 * mate + (lane >> 3), i = 0; i < 4; ++i, q += 4)
+                        if (live[half] >> q & 1)
+                            *reinterpret_cast<uint4 *>((uint8_t *)a.out + ((size_t)row0 + 32 * half + q) * (2 * D) + 256 * c +
+                                                       128 * group + 16 * (lane & 7)) =
+                                *reinterpret_cast<const uint4 *>(box + q * 128 + (((lane & 7) ^ (q & 7)) << 4));
+                }
+            }
+        }
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m->o_empty);
+    }
+    bulk_wait();
+}
+
 template <bool SPLIT_P>
 __device__ void softmax(const Args &a, Misc *m, uint8_t *sm)
 {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int row = tid & (KT - 1), half = tid >> 7;                   // key of the tile, 32 of its 64 rows
     const uint32_t tb = m->tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const float sl = a.scale * LOG2E;
+    const float sl = a.scale == 0.0f ? 1e-30f : a.scale * LOG2E;       // not 0: a masked score stays -inf
+    const float masked = sl > 0.0f ? -INFINITY : INFINITY;
     uint8_t *P = sm + P_OFF;
-    float *red = reinterpret_cast<float *>(P);                         // [4][RT], while P is not in use
-    uint8_t *bad_key = P + 4 * RT * 4;                                 // [2][KT], likewise
+    uint8_t *bad_key = P;                                              // [2][KT], while P is not in use
+    const float4 *muse4 = reinterpret_cast<const float4 *>(m->muse + 32 * half);
     uint32_t unit = 0;
     for (uint32_t s = 0;; ++s) {
         const uint32_t r = s & 1;
-        if (soft_any(!wait(m, &m->seg_full[r], (s >> 1) & 1))) return;  // all eight warps leave, or none
+        if (soft_any(!wait(m, &m->seg_full[r], (s >> 1) & 1))) break;  // all eight warps leave, or none; fac, muse, P are free
         const Segment g = m->seg[r];
-        if (g.tile < 0) return;
+        if (g.tile < 0) break;
         const int *lo = m->lo[r] + 32 * half, *hi = m->hi[r] + 32 * half;
         float l[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) l[j] = 0.0f;
-        if (tid < RT) {
-            m->muse[tid] = 0.0f;
-            m->lim[tid] = -INFINITY;
-        }
-        soft_sync();
+        if (!g.uniform && tid < RT) m->muse[tid] = FRESH;
 
-        int key0 = g.key0, first_row = 0;
-        for (int k = 0; k < g.n; ++k, ++unit, key0 = next_tile(m->lo[r], m->hi[r], key0, first_row)) {
+        int key0 = g.key0;
+        for (int k = 0; k < g.n; ++k, ++unit, key0 = next_tile(g, m->lo[r], m->hi[r], key0)) {
             wait(m, &m->s_full, unit & 1);                             // given up: finish the segment, then leave
             fence_after_sync();
             float x[32];
@@ -374,80 +529,104 @@ __device__ void softmax(const Args &a, Misc *m, uint8_t *sm)
                 tmem_ld32(tb + S_COL + 32 * half, raw);
                 tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(raw[j]) * sl;
+                for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(raw[j]);
             }
-            const int key = key0 + row;
-            bool poison = false;                                       // this key's latent is not finite
             if (key0 < g.max_lo || key0 + KT > g.min_hi) {
                 // A latent that is not finite gives no finite score at all.
                 // A masked weight of zero would not keep it out of O, so it
                 // is cleared, and the rows that do see it become NaN.
-                bool all = true;
+                const int key = key0 + row;
+                float least = INFINITY;
 #pragma unroll
-                for (int j = 0; j < 32; ++j) all &= !(fabsf(x[j]) < INFINITY);
+                for (int j = 0; j < 32; ++j) least = fminf(least, fabsf(x[j]));
+                const bool all = !(least < INFINITY);
+                bool poison = false;                                   // this key's latent is not finite
                 if (soft_any(all)) {
                     bad_key[half * KT + row] = all;
                     soft_sync();
                     poison = bad_key[row] && bad_key[KT + row];
                     soft_sync();
                     if (poison)
-#pragma unroll
+#pragma unroll 1
                         for (int i = 0; i < 4; ++i)
-#pragma unroll
+#pragma unroll 1
                             for (int c = 0; c < 8; ++c)
                                 *reinterpret_cast<uint4 *>(sm + K_OFF + (4 * half + i) * K_SLAB + row * 128 + 16 * c) =
                                     make_uint4(0, 0, 0, 0);
                 }
+                if (g.uniform) {                                       // one token's rows: the key is seen by all or none
+                    if (poison || key < g.max_lo || key >= g.min_hi) {
+                        const float v = key < g.max_lo || key >= g.min_hi ? masked : NAN;
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    if (poison) x[j] = NAN;
-                    if (key < lo[j] || key >= hi[j]) x[j] = -INFINITY;
+                        for (int j = 0; j < 32; ++j) x[j] = v;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        if (poison) x[j] = NAN;
+                        if (key < lo[j] || key >= hi[j]) x[j] = masked;
+                    }
                 }
             }
-            bool rise = false;
+            // A row's first reference: any score near the maximum will do, so
+            // where all rows see the same keys the first of them gives it.
+            if (k == 0 && g.uniform) {
+                if (row == max(key0, g.max_lo) - key0)
 #pragma unroll
-            for (int j = 0; j < 32; ++j) rise |= x[j] - m->muse[32 * half + j] > m->lim[32 * half + j];
-            if (soft_any(rise)) {
+                    for (int j = 0; j < 32; ++j) m->muse[32 * half + j] = x[j] * sl;
+                soft_sync();
+            }
+            bool rise = k == 0 && !g.uniform;
+            if (!rise) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float4 mu = muse4[j];
+                    top = fmaxf(fmaxf(top, fmaf(x[4 * j], sl, -mu.x)), fmaf(x[4 * j + 1], sl, -mu.y));
+                    top = fmaxf(fmaxf(top, fmaf(x[4 * j + 2], sl, -mu.z)), fmaf(x[4 * j + 3], sl, -mu.w));
+                }
+                rise = soft_any(top > RISE);
+            }
+            if (rise) {
                 float v[32];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = x[j];
-                red[(warp & 3) * RT + 32 * half + lane] = columns<true>(v);
+                for (int j = 0; j < 32; ++j) v[j] = x[j] * sl;
+                m->red[warp & 3][32 * half + lane] = columns<true>(v);
                 soft_sync();
                 if (tid < RT) {
-                    const float top = fmaxf(fmaxf(red[tid], red[RT + tid]), fmaxf(red[2 * RT + tid], red[3 * RT + tid]));
-                    const bool fresh = m->lim[tid] == -INFINITY;        // no key seen so far
-                    const float old = fresh ? -INFINITY : m->muse[tid], now = fmaxf(old, top);
-                    m->fac[tid] = now == -INFINITY ? 1.0f : ex2(old - now);
-                    m->muse[tid] = now == -INFINITY ? 0.0f : now;
-                    m->lim[tid] = now == -INFINITY ? -INFINITY : RISE;
+                    const float top = fmaxf(fmaxf(m->red[0][tid], m->red[1][tid]), fmaxf(m->red[2][tid], m->red[3][tid]));
+                    const float old = m->muse[tid], now = fmaxf(old, top);
+                    m->fac[r][tid] = ex2(old - now);                      // fresh and still fresh: 1; now seen: 0
+                    m->muse[tid] = now;
                 }
                 soft_sync();
                 if (k > 0) {                                           // S follows the last O product: O is at rest
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) l[j] *= m->fac[32 * half + j];
+                    for (int j = 0; j < 32; ++j) l[j] *= m->fac[r][32 * half + j];
+#pragma unroll 1
                     for (int c = 0; c < CHUNKS; ++c) {
                         uint32_t o[32];
                         tmem_ld32(tb + O_COL + RT * c + 32 * half, o);
                         tmem_ld_wait();
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            o[j] = __float_as_uint(__uint_as_float(o[j]) * m->fac[32 * half + j]);
+                            o[j] = __float_as_uint(__uint_as_float(o[j]) * m->fac[r][32 * half + j]);
                         tmem_st32(tb + O_COL + RT * c + 32 * half, o);
                     }
                     tmem_st_wait();
                 }
             }
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                x[j] = ex2(x[j] - m->muse[32 * half + j]);
-                l[j] += x[j];
-            }
-#pragma unroll
             for (int c = 0; c < 4; ++c) {
+                const float4 ma = muse4[2 * c], mb = muse4[2 * c + 1];
+                const float mu[8] = {ma.x, ma.y, ma.z, ma.w, mb.x, mb.y, mb.z, mb.w};
                 uint32_t h[4], e[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float p0 = x[8 * c + 2 * i], p1 = x[8 * c + 2 * i + 1];
+                    const float p0 = ex2(fmaf(x[8 * c + 2 * i], sl, -mu[2 * i]));
+                    const float p1 = ex2(fmaf(x[8 * c + 2 * i + 1], sl, -mu[2 * i + 1]));
+                    l[8 * c + 2 * i] += p0;
+                    l[8 * c + 2 * i + 1] += p1;
                     h[i] = pack2(p0, p1);
                     if (SPLIT_P) e[i] = pack2(p0 - __uint_as_float(h[i] << 16), p1 - __uint_as_float(h[i] & 0xffff0000u));
                 }
@@ -461,57 +640,24 @@ __device__ void softmax(const Args &a, Misc *m, uint8_t *sm)
             if (lane == 0) mbar_arrive(&m->p_full);
         }
 
-        // ---- output
-        wait(m, &m->o_full, s & 1);
-        fence_after_sync();
-        red[(warp & 3) * RT + 32 * half + lane] = columns<false>(l);
+        // ---- the rows' sums
+        m->red[warp & 3][32 * half + lane] = columns<false>(l);
         soft_sync();
         const int64_t row0 = (int64_t)g.tile * RT;
         if (tid < RT) {
-            const float sum = (red[tid] + red[RT + tid]) + (red[2 * RT + tid] + red[3 * RT + tid]);
-            const bool none = m->lim[tid] == -INFINITY && !(sum != sum);   // no key seen (a NaN sum has seen one)
+            const float sum = (m->red[0][tid] + m->red[1][tid]) + (m->red[2][tid] + m->red[3][tid]);
+            const bool none = m->muse[tid] == FRESH && !(sum != sum);  // no key seen (a NaN sum has seen one)
             if (g.slot >= 0) {
                 a.part_ml[(size_t)g.slot * RT + tid] = make_float2(none ? -INFINITY : m->muse[tid], none ? 0.0f : sum);
             } else {
-                m->fac[tid] = none ? 0.0f : 1.0f / sum;
+                m->fac[r][tid] = none ? 0.0f : 1.0f / sum;
                 if (a.lse && m->hi[r][tid] >= 0)
                     a.lse[row0 + tid] = none ? -INFINITY : (m->muse[tid] + log2f(sum)) * LN2;
             }
         }
-        soft_sync();
-        const bool bf16 = !SPLIT_P && g.slot < 0;
-        float *out_f = g.slot >= 0 ? a.part_o + (size_t)g.slot * RT * D : (float *)a.out + row0 * D;
-        __nv_bfloat16 *out_h = (__nv_bfloat16 *)a.out + row0 * D;
-        for (int c = 0; c < CHUNKS; ++c) {
-            uint32_t o[32];
-            tmem_ld32(tb + O_COL + RT * c + 32 * half, o);
-            tmem_ld_wait();
-            const int d = 128 * c + (row & 127);
-            if (bf16) {
-#pragma unroll
-                for (int j = 0; j < 32; j += 2) {                      // neighbours swap: two channels of one row each
-                    const int q0 = 32 * half + j;
-                    const float v0 = __uint_as_float(o[j]) * m->fac[q0], v1 = __uint_as_float(o[j + 1]) * m->fac[q0 + 1];
-                    const bool odd = lane & 1;
-                    const float got = __shfl_xor_sync(~0u, odd ? v0 : v1, 1);
-                    const int q = q0 + odd;
-                    if (m->hi[r][q] >= 0)
-                        *reinterpret_cast<uint32_t *>(out_h + (size_t)q * D + (d & ~1)) =
-                            odd ? pack2(got, v1) : pack2(v0, got);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const int q = 32 * half + j;
-                    if (m->hi[r][q] >= 0)
-                        out_f[(size_t)q * D + d] = __uint_as_float(o[j]) * (g.slot >= 0 ? 1.0f : m->fac[q]);
-                }
-            }
-        }
-        fence_before_sync();
         __syncwarp();
+        if (lane == 0 && warp < RT / 32) mbar_arrive(&m->fac_full[r]);
         if (lane == 0) mbar_arrive(&m->seg_empty[r]);
-        soft_sync();                                                   // fac, muse and P's scratch are free again
     }
 }
 
@@ -529,12 +675,13 @@ __device__ void deal_units(const Args &a, Misc *m, int *before)
         const int y = __shfl_up_sync(~0u, x, d);
         if (lane >= d) x += y;
     }
-    if (lane == 31) m->scan[warp] = x;
+    int *sums = reinterpret_cast<int *>(m->red);
+    if (lane == 31) sums[warp] = x;
     __syncthreads();
     int add = 0, total = 0;
     for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) add += m->scan[w];
-        total += m->scan[w];
+        if (w < warp) add += sums[w];
+        total += sums[w];
     }
     const int mine = add + x - n[0] - n[1];
     if (2 * tid < a.tiles) before[2 * tid] = mine;
@@ -563,16 +710,17 @@ __device__ void deal_units(const Args &a, Misc *m, int *before)
 
 template <bool SPLIT_P, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 1)
-prompt_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k, const Args a)
+prompt_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                     const __grid_constant__ CUtensorMap map_out, const Args a)
 {
     extern __shared__ __align__(1024) uint8_t sm[];
-    Misc *m = reinterpret_cast<Misc *>(sm + P_OFF + (SPLIT_P ? 2 : 1) * P_BYTES);
+    Misc *m = reinterpret_cast<Misc *>(sm + P_OFF + 2 * P_BYTES);
     const int tid = threadIdx.x, warp = tid >> 5;
     if (smem_addr(sm) & 1023) {                                        // the swizzled tiles need it
         if (tid == 0) set_error(a.error, CSA2_DEV_BAD_REQUEST);
         return;
     }
-    if (warp == SOFT_WARPS + 1) tmem_alloc(&m->tmem, TMEM_COLS);
+    if (warp == MMA_WARP) tmem_alloc(&m->tmem, TMEM_COLS);
     if (tid == 0) {
         mbar_init(&m->q_full, 1);
         mbar_init(&m->q_empty, 1);
@@ -583,15 +731,18 @@ prompt_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         mbar_init(&m->s_full, 1);
         mbar_init(&m->p_full, SOFT_WARPS);
         mbar_init(&m->o_full, 1);
+        mbar_init(&m->o_empty, STORE_WARPS);
         mbar_init(&m->drain, 1);
         for (int r = 0; r < 2; ++r) {
             mbar_init(&m->seg_full[r], 1);
-            mbar_init(&m->seg_empty[r], SOFT_WARPS + 1);
+            mbar_init(&m->seg_empty[r], SOFT_WARPS + STORE_WARPS + 1);
+            mbar_init(&m->fac_full[r], RT / 32);
         }
         mbar_fence_init();
         m->abort = 0;
         tma_prefetch_map(&map_q);
         tma_prefetch_map(&map_k);
+        tma_prefetch_map(&map_out);
     }
     grid_dependency_wait();
     allow_dependents();
@@ -607,11 +758,13 @@ prompt_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
 
     if (warp < SOFT_WARPS) {
         softmax<SPLIT_P>(a, m, sm);
-    } else if (warp == SOFT_WARPS) {
+    } else if (warp < LOAD_WARP) {
+        store<SPLIT_P>(a, m, sm + P_OFF + P_BYTES, &map_out);
+    } else if (warp == LOAD_WARP) {
         if (SPLIT) fence_proxy_async_smem();                           // the plan's scratch lies where the latents land
         producer<SPLIT>(a, m, sm, &map_q, &map_k);
     } else {
-        if ((tid & 31) == 0) {
+        if (elect_one()) {                                             // not a lane test: MMAs issue from uniform registers
             mma_issuer<SPLIT_P>(m, sm);
             mma_commit(&m->drain);                                     // no MMA may be in flight at exit
             mbar_wait(&m->drain, 0);
@@ -621,53 +774,71 @@ prompt_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     fence_before_sync();
     __syncthreads();
     if (tid == 0 && m->abort) set_error(a.error, CSA2_DEV_TIMEOUT);
-    if (warp == SOFT_WARPS + 1) {
+    if (warp == MMA_WARP) {
         fence_after_sync();
         tmem_dealloc(m->tmem, TMEM_COLS);
     }
 }
 
-// Joins the parts of the row tiles that several CTAs of `grid` shared; one row per CTA.
+// Joins the parts of the row tiles that several CTAs of `grid` shared; four rows per CTA.
 template <bool F32>
-__global__ void __launch_bounds__(D / 4) prompt_join_kernel(const Args a, int grid)
+__global__ void __launch_bounds__(128) prompt_join_kernel(const Args a, int grid)
 {
     grid_dependency_wait();
     allow_dependents();
-    const int tile = blockIdx.x / RT, i = blockIdx.x % RT;
+    const int tile = blockIdx.x / (RT / 4), i = 4 * (blockIdx.x % (RT / 4));
+    const int c = blockIdx.y, d = 128 * c + threadIdx.x;
     const int64_t total = a.prefix[a.tiles], u0 = a.prefix[tile], u1 = a.prefix[tile + 1];
-    const int64_t row = (int64_t)tile * RT + i;
-    if (u1 == u0 || row / a.heads >= live_tokens(a)) return;
+    const int64_t row = (int64_t)tile * RT + i, live = (int64_t)live_tokens(a) * a.heads;
+    if (u1 == u0 || row >= live) return;
     const int64_t ctas = min((int64_t)grid, total);
     const int c0 = (int)(((u0 + 1) * ctas - 1) / total), c1 = (int)((u1 * ctas - 1) / total);
     if (c0 == c1) return;                                              // one CTA had all of it
-    // A CTA keeps the part of the row tile that it began with in its first slot, a later one in its second.
-    auto slot = [&](int c) { return (size_t)2 * c + (total * c / ctas >= u0 ? 0 : 1); };
-    float top = -INFINITY;
-    for (int c = c0; c <= c1; ++c) top = fmaxf(top, a.part_ml[slot(c) * RT + i].x);
-    float sum = 0.0f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = c0; c <= c1; ++c) {
-        const float2 ml = a.part_ml[slot(c) * RT + i];
-        if (ml.x == -INFINITY) continue;
-        const float w = ex2(ml.x - top);
-        const float4 v = *reinterpret_cast<const float4 *>(a.part_o + (slot(c) * RT + i) * D + 4 * threadIdx.x);
-        sum += w * ml.y;
-        o.x += w * v.x;
-        o.y += w * v.y;
-        o.z += w * v.z;
-        o.w += w * v.w;
+    // A CTA keeps the part of the row tile that it began with in its first
+    // slot, a later one in its second; only the first of these CTAs began before.
+    const size_t first = 2 * (size_t)c0 + (total * c0 / ctas >= u0 ? 0 : 1);
+    const int n = c1 - c0 + 1;
+    __shared__ float weight[4][CTAS], inv[4];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    {                                                                  // warp w: weights of row i + w
+        float top = -INFINITY, sum = 0.0f;
+        for (int k = lane; k < n; k += 32)
+            top = fmaxf(top, a.part_ml[(k ? 2 * (size_t)(c0 + k) : first) * RT + i + warp].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+        for (int k = lane; k < n; k += 32) {
+            const float2 ml = a.part_ml[(k ? 2 * (size_t)(c0 + k) : first) * RT + i + warp];
+            const float w = ml.x == -INFINITY ? 0.0f : ex2(ml.x - top);
+            weight[warp][k] = w;
+            if (ml.x != -INFINITY) sum += w * ml.y;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        if (lane == 0) {
+            const bool none = top == -INFINITY;
+            inv[warp] = none ? 0.0f : 1.0f / sum;
+            if (c == 0 && a.lse && row + warp < live) a.lse[row + warp] = none ? -INFINITY : (top + log2f(sum)) * LN2;
+        }
     }
-    const bool none = top == -INFINITY;
-    const float f = none ? 0.0f : 1.0f / sum;
-    const size_t at = (size_t)row * D + 4 * threadIdx.x;
-    if (F32)
-        *reinterpret_cast<float4 *>((float *)a.out + at) = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-    else
-        *reinterpret_cast<uint2 *>((__nv_bfloat16 *)a.out + at) = make_uint2(pack2(o.x * f, o.y * f), pack2(o.z * f, o.w * f));
-    if (a.lse && threadIdx.x == 0) a.lse[row] = none ? -INFINITY : (top + log2f(sum)) * LN2;
+    __syncthreads();
+    float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+        const float4 v = *reinterpret_cast<const float4 *>(a.part_o + (k ? 2 * (size_t)(c0 + k) : first) * RT * D + part_at(i, d));
+        o[0] += weight[0][k] * v.x;
+        o[1] += weight[1][k] * v.y;
+        o[2] += weight[2][k] * v.z;
+        o[3] += weight[3][k] * v.w;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (row + j >= live) break;
+        const size_t at = (size_t)(row + j) * D + d;
+        if (F32) ((float *)a.out)[at] = o[j] * inv[j];
+        else ((__nv_bfloat16 *)a.out)[at] = __float2bfloat16_rn(o[j] * inv[j]);
+    }
 }
 
-constexpr int CTAS = 148;                      // one per SM
 constexpr int SLOTS = 2 * CTAS;
 
 struct Layout {
@@ -684,22 +855,26 @@ constexpr Layout layout()
 
 int64_t row_tiles(int64_t n_q, int heads) { return (n_q * heads + RT - 1) / RT; }
 
-// [rows][512] bf16 in boxes of 64 channels x box_rows, 128-byte swizzled.
-bool make_map(CUtensorMap *m, const void *p, int64_t rows, int64_t stride, int box_rows)
+// [rows][512] bf16 as 8 slabs of 64 channels, in boxes of box_rows x box_slabs
+// that land slab by slab, 128-byte swizzled.  One load brings a whole chunk:
+// a thread gets a load out every 150 cycles at best, and slab by slab the
+// loop around them held a key tile back to 3200 cycles, against 1800 for
+// 128 KB from L2 into every SM at once.
+bool make_map(CUtensorMap *m, const void *p, int64_t rows, int64_t stride, int box_rows, int box_slabs)
 {
     auto fn = tensor_map_encoder();
     if (!fn) return false;
-    cuuint64_t dims[2] = {D, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
-    cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
-    cuuint32_t estr[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (void *)p, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    cuuint64_t dims[3] = {64, (cuuint64_t)rows, D / 64};
+    cuuint64_t strides[2] = {(cuuint64_t)stride * 2, 128};
+    cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_slabs};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, (void *)p, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
            CUDA_SUCCESS;
 }
 
 template <bool SPLIT_P, bool SPLIT>
-cudaError_t launch_variant(const CUtensorMap &map_q, const CUtensorMap &map_k, const Args &a, int grid, cudaStream_t st)
+cudaError_t launch_variant(const CUtensorMap &map_q, const CUtensorMap &map_k, const CUtensorMap &map_out, const Args &a, int grid, cudaStream_t st)
 {
     static DeviceOnce once;
     int dev = 0;
@@ -707,16 +882,16 @@ cudaError_t launch_variant(const CUtensorMap &map_q, const CUtensorMap &map_k, c
     if (e == cudaSuccess)
         e = once.run(dev, [] {
             return cudaFuncSetAttribute(prompt_attend_kernel<SPLIT_P, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        (int)smem_bytes(SPLIT_P));
+                                        (int)SMEM_BYTES);
         });
     if (e != cudaSuccess) return e;
     {
         LaunchScope scope(-1, st);
-        e = launch_pdl(prompt_attend_kernel<SPLIT_P, SPLIT>, dim3(grid), dim3(THREADS), smem_bytes(SPLIT_P), st, map_q, map_k, a);
+        e = launch_pdl(prompt_attend_kernel<SPLIT_P, SPLIT>, dim3(grid), dim3(THREADS), SMEM_BYTES, st, map_q, map_k, map_out, a);
     }
     if (e != cudaSuccess || !SPLIT) return e;
     LaunchScope scope(-1, st);
-    return launch_pdl(prompt_join_kernel<SPLIT_P>, dim3(a.tiles * RT), dim3(D / 4), 0, st, a, grid);
+    return launch_pdl(prompt_join_kernel<SPLIT_P>, dim3(a.tiles * (RT / 4), CHUNKS), dim3(128), 0, st, a, grid);
 }
 
 }  // namespace
@@ -746,19 +921,20 @@ cudaError_t launch_prompt_attend(const PromptArgs &p, cudaStream_t st)
     a.part_o = (float *)((char *)p.ws + l.o);
     a.part_ml = (float2 *)((char *)p.ws + l.ml);
     a.prefix = (int32_t *)((char *)p.ws + l.prefix);
-    CUtensorMap map_q, map_k;
+    CUtensorMap map_q, map_k, map_out;
     // Without keys the latents' map covers a row of q that every mask leaves out.
-    if (!make_map(&map_q, p.q, (int64_t)p.n_q * p.heads, D, RT) ||
-        !make_map(&map_k, p.n_k ? p.lat : p.q, p.n_k ? p.n_k : 1, p.n_k ? p.lat_stride : D, KT))
+    if (!make_map(&map_q, p.q, (int64_t)p.n_q * p.heads, D, RT, 8) ||
+        !make_map(&map_out, p.out, (int64_t)p.n_q * p.heads, D, RT / 2, 1) ||        // f32 outputs do not use it
+        !make_map(&map_k, p.n_k ? p.lat : p.q, p.n_k ? p.n_k : 1, p.n_k ? p.lat_stride : D, KT, 2))
         return cudaErrorInvalidValue;
     // Row tiles of one key tile each cannot be shared; many fill the SMs as they are.
     const bool one = p.n_k <= KT || (p.window > 0 && p.window <= KT && p.heads % RT == 0);
     if (!one && a.tiles <= MAX_SPLIT_TILES)
-        return p.out_is_fp32 ? launch_variant<true, true>(map_q, map_k, a, CTAS, st)
-                             : launch_variant<false, true>(map_q, map_k, a, CTAS, st);
+        return p.out_is_fp32 ? launch_variant<true, true>(map_q, map_k, map_out, a, CTAS, st)
+                             : launch_variant<false, true>(map_q, map_k, map_out, a, CTAS, st);
     const int grid = std::min(a.tiles, CTAS);
-    return p.out_is_fp32 ? launch_variant<true, false>(map_q, map_k, a, grid, st)
-                         : launch_variant<false, false>(map_q, map_k, a, grid, st);
+    return p.out_is_fp32 ? launch_variant<true, false>(map_q, map_k, map_out, a, grid, st)
+                         : launch_variant<false, false>(map_q, map_k, map_out, a, grid, st);
 }
 
 }  // namespace csa2
