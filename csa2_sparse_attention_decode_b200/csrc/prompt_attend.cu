@@ -62,12 +62,21 @@ constexpr float FRESH = -3.0e38f;              // reference of a row that has se
 constexpr int CTAS = 148;                      // one per SM
 constexpr int MAX_SPLIT_TILES = 2 * THREADS;   // row tiles that the split path plans in every CTA
 
+// How row tiles meet the CTAs.
+enum Deal {
+    WHOLE,                                     // round robin
+    SHARED,                                    // (row tile, key tile) units evenly: a row tile may have several CTAs
+    SLIDING                                    // runs of single-token row tiles whose keys fit one key tile
+};
+
 struct Segment {                               // n consecutive key tiles of one row tile
-    int tile, n, key0;                         // key0: first key of the first of them
+    int tile, n, key0;                         // key0: first key of the first of them; key key0 + i lies in row
+                                               // (i + turn) % 128 of the tile
     int max_lo, min_hi;                        // keys in [max_lo, min_hi) are seen by every live row
     int slot;                                  // partial result's slot, -1: the segment is the whole row tile
     bool uniform;                              // every row sees [max_lo, min_hi), which is not empty
     bool boxed;                                // every row that exists belongs to a request
+    uint8_t turn;
 };
 
 struct Misc {
@@ -77,15 +86,21 @@ struct Misc {
     alignas(16) float muse[RT], red[4][RT], fac[2][RT];
     uint32_t tmem;
     int abort;
-    int64_t n_units;                           // split path: this CTA's share
-    int first_tile, first_at;
+    uint32_t cleared[KT / 32];                 // SLIDING: latents that were not finite and lie in the tile as zeros
 };
 constexpr size_t SMEM_BYTES = P_OFF + 2 * P_BYTES + sizeof(Misc);
 static_assert(SMEM_BYTES <= 232448, "shared memory of one CTA");
 
+struct Share {                                 // SHARED: what deal_units() leaves for the producer, in Misc::red
+    int64_t units;
+    int tile, at;
+};
+
 struct Args {
     const int32_t *cu_q, *cu_k;
     int batch, n_q, n_k, heads, window, tiles;
+    const uint16_t *lat;
+    int64_t lat_stride;
     float scale;
     void *out;
     float *lse;
@@ -182,7 +197,10 @@ __device__ __forceinline__ bool warp_wait(Misc *m, uint64_t *bar, uint32_t parit
     return __all_sync(~0u, wait(m, bar, parity));
 }
 
-// True in one lane of a converged warp.
+// True in one lane of a converged warp, the same each time.  Loads, stores and
+// MMAs issue from uniform registers: behind a test of the lane number the
+// compiler cannot see that one lane is left, and each issue costs hundreds of
+// cycles more.
 __device__ __forceinline__ bool elect_one()
 {
     uint32_t r;
@@ -244,18 +262,30 @@ __device__ __forceinline__ float columns(float (&v)[32])
 
 // ------------------------------------------------------------------ roles
 // Plans the CTA's segments and loads their queries and latents.
-template <bool SPLIT>
+//
+// SLIDING: a token's keys are the last token's, one in and one out.  The tile
+// is a ring then: key k lies in row (k - base) % 128, the new latent goes
+// over the one that left, and 1 KB comes in a token instead of 128 KB.
+template <Deal DEAL>
 __device__ void producer(const Args &a, Misc *m, uint8_t *sm, const CUtensorMap *map_q, const CUtensorMap *map_k)
 {
     const int lane = threadIdx.x & 31;
     const int live = live_tokens(a);
-    int tile = SPLIT ? m->first_tile : a.tiles - 1 - (int)blockIdx.x, at = SPLIT ? m->first_at : 0;
-    int64_t left = SPLIT ? m->n_units : 0;
-    uint32_t unit = 0, s = 0;
-    for (;; ++s) {
-        Segment g = {-1, 0, 0, 0, 0, -1, false, false};
-        if (SPLIT) {
-            for (; left > 0 && tile < a.tiles; ++tile, at = 0) {
+    const Share share = *reinterpret_cast<const Share *>(m->red);
+    int tile = blockIdx.x, at = 0, last = a.tiles;
+    if (DEAL == WHOLE) tile = a.tiles - 1 - tile;                      // later tokens see more: heavy row tiles first
+    if (DEAL == SHARED) tile = share.tile, at = share.at;
+    if (DEAL == SLIDING) {
+        tile = (int)((int64_t)a.tiles * blockIdx.x / gridDim.x);
+        last = (int)((int64_t)a.tiles * (blockIdx.x + 1) / gridDim.x);
+    }
+    int64_t left = DEAL == SHARED ? share.units : 0;
+    int base = 0, top = -1;                                            // SLIDING: the ring holds keys [top - 128, top)
+    uint32_t unit = 0;
+    for (uint32_t s = 0;; ++s) {
+        Segment g = {-1, 0, 0, 0, 0, -1, false, false, 0};
+        if (DEAL == SHARED) {
+            for (; left > 0 && tile < last; ++tile, at = 0) {
                 const int total = key_tiles(a, live, tile, at, g.key0);
                 if (total - at <= 0) continue;
                 g.tile = tile;
@@ -266,7 +296,7 @@ __device__ void producer(const Args &a, Misc *m, uint8_t *sm, const CUtensorMap 
                 at = 0;
                 break;
             }
-        } else {
+        } else if (DEAL == WHOLE) {
             for (; tile >= 0; tile -= gridDim.x) {
                 const int total = key_tiles(a, live, tile, 0, g.key0);
                 if (total == 0) continue;
@@ -275,6 +305,9 @@ __device__ void producer(const Args &a, Misc *m, uint8_t *sm, const CUtensorMap 
                 tile -= gridDim.x;
                 break;
             }
+        } else if (tile < last && tile * RT / a.heads < live) {
+            g.tile = tile++;
+            g.n = 1;
         }
         int lo[2] = {0, 0}, hi[2] = {-1, -1};                          // hi < 0: no such row
         if (g.tile >= 0) {
@@ -296,6 +329,26 @@ __device__ void producer(const Args &a, Misc *m, uint8_t *sm, const CUtensorMap 
             g.uniform = __reduce_min_sync(~0u, min_lo) == g.max_lo && __reduce_max_sync(~0u, max_hi) == g.min_hi && g.min_hi > 0;
             g.boxed = (int64_t)live * a.heads >= min((int64_t)(g.tile + 1) * RT, (int64_t)a.n_q * a.heads);
         }
+        // SLIDING: what the ring lacks: nothing, the latent that follows, or all
+        bool refill = true;
+        int fresh = -1;                                                // ring row of the one latent
+        uint4 latent[2];
+        if (DEAL == SLIDING && g.tile >= 0) {
+            refill = top < 0 || g.max_lo < top - KT || g.min_hi > top + 1 || (g.min_hi > top && g.max_lo == top - KT);
+            if (refill) {
+                base = g.max_lo;
+                top = base + KT;
+            } else if (g.min_hi > top) {
+                // lanes 0-15 hold 16 bytes each of chunks 0 and 2, the others of chunks 1 and 3
+                const uint4 *src = reinterpret_cast<const uint4 *>(a.lat + (size_t)top * a.lat_stride) + lane;
+                latent[0] = __ldg(src);
+                latent[1] = __ldg(src + 32);
+                fresh = (top - base) & (KT - 1);
+                ++top;
+            }
+            g.key0 = top - KT;
+            g.turn = (uint8_t)((g.key0 - base) & (KT - 1));
+        }
         const uint32_t r = s & 1;
         bool ok = warp_wait(m, &m->seg_empty[r], ((s >> 1) & 1) ^ 1);
         if (ok) {
@@ -311,17 +364,31 @@ __device__ void producer(const Args &a, Misc *m, uint8_t *sm, const CUtensorMap 
         if (ok && g.tile < 0) return;
 
         ok = ok && warp_wait(m, &m->q_empty, (s & 1) ^ 1);
-        if (ok && lane == 0) {
+        if (ok && elect_one()) {
             mbar_arrive_expect_tx(&m->q_full, 8 * Q_SLAB);
             tma_load_3d(sm + Q_OFF, map_q, 0, g.tile * RT, 0, &m->q_full);
         }
-        int key0 = g.key0;
+        int key0 = DEAL == SLIDING ? base : g.key0;
         for (int k = 0; ok && k < g.n; ++k, ++unit, key0 = next_tile(g, m->lo[r], m->hi[r], key0)) {
 #pragma unroll 1
             for (int c = 0; c < CHUNKS; ++c) {
                 ok = warp_wait(m, &m->k_empty[c], (unit & 1) ^ 1);
                 if (!ok) break;
-                if (lane == 0) {
+                if (DEAL == SLIDING && c == 0 && lane < KT / 32) {     // read before the products that are done now
+                    if (refill) m->cleared[lane] = 0;
+                    else if (fresh >= 0 && lane == fresh >> 5) m->cleared[lane] &= ~(1u << (fresh & 31));
+                }
+                __syncwarp();
+                if (!refill) {
+                    if (fresh >= 0 && lane >> 4 == (c & 1)) {
+                        const int piece = lane & 15;
+                        *reinterpret_cast<uint4 *>(sm + K_OFF + (2 * c + (piece >> 3)) * K_SLAB + fresh * 128 +
+                                                   (((piece & 7) ^ (fresh & 7)) << 4)) = latent[c >> 1];
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&m->k_full[c]);
+                } else if (elect_one()) {
                     mbar_arrive_expect_tx(&m->k_full[c], 2 * K_SLAB);
                     tma_load_3d(sm + K_OFF + 2 * c * K_SLAB, map_k, 0, key0, 2 * c, &m->k_full[c]);
                 }
@@ -402,12 +469,19 @@ __device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&r)[16])
                  : "r"(taddr));
 }
 
+// One warp has all of O that it stores in registers.
+__device__ __forceinline__ void o_read(Misc *m)
+{
+    fence_before_sync();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&m->o_empty);
+}
+
 // The output of a row tile, by four warps of their own: warp w takes channels
 // 32 w .. 32 w + 31 of every chunk while the others are at the next row tile.
 //
-// bf16: O is turned round with stmatrix into boxes of 64 channels x 32 rows,
-// which two warps fill and a bulk store takes away; four such boxes are in
-// turn.  (Element stores of the same lines, shuffled or staged, took 5500
+// bf16: O is turned round with stmatrix into boxes of 64 channels x 64 rows,
+// which two warps fill and a bulk store takes away.  (Element stores of the same lines, shuffled or staged, took 5500
 // cycles a row tile: the next S leaves the shared-memory pipe little time.)
 // f32: a warp's 32 channels are a line, stored as they are.
 // A part keeps f32 sums, four rows side by side.
@@ -415,7 +489,6 @@ template <bool SPLIT_P>
 __device__ void store(const Args &a, Misc *m, uint8_t *stage, const CUtensorMap *map_out)
 {
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3, mate = w & 1, group = w >> 1;
-    const bool storer = lane == 0 && mate == 0;
     const uint32_t tb = m->tmem + ((uint32_t)(32 * w) << 16) + O_COL;
     // matrix lane / 8 of a stmatrix: 8 channels, x the 8 rows whose addresses the lanes give
     const int put = (lane & 7) * 128 + (((4 * mate + (lane >> 3)) ^ (lane & 7)) << 4);
@@ -439,6 +512,7 @@ __device__ void store(const Args &a, Misc *m, uint8_t *stage, const CUtensorMap 
                 uint32_t o[32];
                 tmem_ld32(tb + RT * c + 32 * half, o);
                 tmem_ld_wait();
+                if (ch == 2 * CHUNKS - 1) o_read(m);
                 if (slot >= 0) {
                     float *part = a.part_o + (size_t)slot * RT * D;
 #pragma unroll
@@ -453,24 +527,24 @@ __device__ void store(const Args &a, Misc *m, uint8_t *stage, const CUtensorMap 
             }
         } else {
 #pragma unroll 1
-            for (int ch = 0; ch < 2 * CHUNKS; ++ch) {
-                const int c = ch >> 1, half = ch & 1;
-                uint32_t lo[16], hi[16];                               // channels 0-15 and 16-31 of the warp's
-                tmem_ld_16x32(tb + RT * c + 32 * half, lo);
-                tmem_ld_16x32(tb + (16u << 16) + RT * c + 32 * half, hi);
+            for (int c = 0; c < CHUNKS; ++c) {
+                uint32_t o[2][2][16];                                  // rows 0-31, 32-63; channels 0-15, 16-31 of the warp's
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    tmem_ld_16x32(tb + ((16u * (i & 1)) << 16) + RT * c + 32 * (i >> 1), o[i >> 1][i & 1]);
                 tmem_ld_wait();
-                uint8_t *box = stage + (2 * group + half) * (32 * 128);
-                if (storer) bulk_wait_read<1>();                       // all but the newest store have read their box
+                if (c == CHUNKS - 1) o_read(m);
+                uint8_t *box = stage + group * (RT * 128);
+                bulk_wait_read<0>();                                   // the last store has read the box
                 group_sync(group);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {                          // rows 8i .. 8i+7
-                    const float2 f = *reinterpret_cast<const float2 *>(fac + 32 * half + 8 * i + 2 * (lane & 3));
+                for (int i = 0; i < 8; ++i) {                          // rows 8i .. 8i+7
+                    const float2 f = *reinterpret_cast<const float2 *>(fac + 8 * i + 2 * (lane & 3));
                     uint32_t v[4];
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        v[k] = pack2(__uint_as_float(lo[4 * i + 2 * k]) * f.x, __uint_as_float(lo[4 * i + 2 * k + 1]) * f.y);
-                        v[2 + k] = pack2(__uint_as_float(hi[4 * i + 2 * k]) * f.x, __uint_as_float(hi[4 * i + 2 * k + 1]) * f.y);
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        v[k] = pack2(__uint_as_float(o[i >> 2][k >> 1][4 * (i & 3) + 2 * (k & 1)]) * f.x,
+                                     __uint_as_float(o[i >> 2][k >> 1][4 * (i & 3) + 2 * (k & 1) + 1]) * f.y);
                     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
                                      smem_addr(box + put) + 1024 * i),
                                  "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
@@ -479,24 +553,22 @@ __device__ void store(const Args &a, Misc *m, uint8_t *stage, const CUtensorMap 
                 fence_proxy_async_smem();
                 group_sync(group);
                 if (boxed) {
-                    if (storer) tma_store_3d(map_out, box, 0, tile * RT + 32 * half, 2 * c + group);
+                    if (mate == 0 && elect_one()) tma_store_3d(map_out, box, 0, tile * RT, 2 * c + group);
                 } else {                                               // some rows belong to no request
-                    for (int q = 16 * mate + (lane >> 3), i = 0; i < 4; ++i, q += 4)
-                        if (live[half] >> q & 1)
-                            *reinterpret_cast<uint4 *>((uint8_t *)a.out + ((size_t)row0 + 32 * half + q) * (2 * D) + 256 * c +
-                                                       128 * group + 16 * (lane & 7)) =
+#pragma unroll 1
+                    for (int q = 32 * mate + (lane >> 3), i = 0; i < 8; ++i, q += 4)
+                        if (live[mate] >> (q & 31) & 1)
+                            *reinterpret_cast<uint4 *>((uint8_t *)a.out + ((size_t)row0 + q) * (2 * D) + 256 * c + 128 * group +
+                                                       16 * (lane & 7)) =
                                 *reinterpret_cast<const uint4 *>(box + q * 128 + (((lane & 7) ^ (q & 7)) << 4));
                 }
             }
         }
-        fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&m->o_empty);
     }
     bulk_wait();
 }
 
-template <bool SPLIT_P>
+template <bool SPLIT_P, Deal DEAL>
 __device__ void softmax(const Args &a, Misc *m, uint8_t *sm)
 {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -531,22 +603,25 @@ __device__ void softmax(const Args &a, Misc *m, uint8_t *sm)
 #pragma unroll
                 for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(raw[j]);
             }
-            if (key0 < g.max_lo || key0 + KT > g.min_hi) {
+            const bool cleared = DEAL == SLIDING && (m->cleared[0] | m->cleared[1] | m->cleared[2] | m->cleared[3]);
+            if (key0 < g.max_lo || key0 + KT > g.min_hi || cleared) {
                 // A latent that is not finite gives no finite score at all.
                 // A masked weight of zero would not keep it out of O, so it
                 // is cleared, and the rows that do see it become NaN.
-                const int key = key0 + row;
+                const int key = key0 + ((row - g.turn) & (KT - 1));
                 float least = INFINITY;
 #pragma unroll
                 for (int j = 0; j < 32; ++j) least = fminf(least, fabsf(x[j]));
                 const bool all = !(least < INFINITY);
-                bool poison = false;                                   // this key's latent is not finite
+                bool poison = cleared && (m->cleared[row >> 5] >> (row & 31) & 1);     // this key's latent is not finite
                 if (soft_any(all)) {
                     bad_key[half * KT + row] = all;
                     soft_sync();
-                    poison = bad_key[row] && bad_key[KT + row];
+                    const bool found = bad_key[row] && bad_key[KT + row];
                     soft_sync();
-                    if (poison)
+                    if (DEAL == SLIDING && found && half == 0) atomicOr(&m->cleared[row >> 5], 1u << (row & 31));
+                    poison |= found;
+                    if (found)
 #pragma unroll 1
                         for (int i = 0; i < 4; ++i)
 #pragma unroll 1
@@ -571,7 +646,7 @@ __device__ void softmax(const Args &a, Misc *m, uint8_t *sm)
             // A row's first reference: any score near the maximum will do, so
             // where all rows see the same keys the first of them gives it.
             if (k == 0 && g.uniform) {
-                if (row == max(key0, g.max_lo) - key0)
+                if (((row - g.turn) & (KT - 1)) == max(key0, g.max_lo) - key0)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) m->muse[32 * half + j] = x[j] * sl;
                 soft_sync();
@@ -702,13 +777,11 @@ __device__ void deal_units(const Args &a, Misc *m, int *before)
             const int mid = (b + e) >> 1;
             if (before[mid] <= u0) b = mid; else e = mid;
         }
-        m->first_tile = b;
-        m->first_at = (int)(u0 - before[b]);
-        m->n_units = u1 - u0;
+        *reinterpret_cast<Share *>(m->red) = {u1 - u0, b, (int)(u0 - before[b])};
     }
 }
 
-template <bool SPLIT_P, bool SPLIT>
+template <bool SPLIT_P, Deal DEAL>
 __global__ void __launch_bounds__(THREADS, 1)
 prompt_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_out, const Args a)
@@ -751,20 +824,20 @@ prompt_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             if ((b == 0 && (a.cu_q[0] != 0 || a.cu_k[0] != 0)) || a.cu_q[b + 1] < a.cu_q[b] || a.cu_k[b + 1] < a.cu_k[b] ||
                 a.cu_q[b + 1] > a.n_q || a.cu_k[b + 1] > a.n_k)
                 set_error(a.error, CSA2_DEV_BAD_REQUEST);
-    if (SPLIT) deal_units(a, m, reinterpret_cast<int *>(sm));
+    if (DEAL == SHARED) deal_units(a, m, reinterpret_cast<int *>(sm));
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
 
     if (warp < SOFT_WARPS) {
-        softmax<SPLIT_P>(a, m, sm);
+        softmax<SPLIT_P, DEAL>(a, m, sm);
     } else if (warp < LOAD_WARP) {
         store<SPLIT_P>(a, m, sm + P_OFF + P_BYTES, &map_out);
     } else if (warp == LOAD_WARP) {
-        if (SPLIT) fence_proxy_async_smem();                           // the plan's scratch lies where the latents land
-        producer<SPLIT>(a, m, sm, &map_q, &map_k);
+        if (DEAL == SHARED) fence_proxy_async_smem();                  // the plan's scratch lies where the latents land
+        producer<DEAL>(a, m, sm, &map_q, &map_k);
     } else {
-        if (elect_one()) {                                             // not a lane test: MMAs issue from uniform registers
+        if (elect_one()) {
             mma_issuer<SPLIT_P>(m, sm);
             mma_commit(&m->drain);                                     // no MMA may be in flight at exit
             mbar_wait(&m->drain, 0);
@@ -873,7 +946,7 @@ bool make_map(CUtensorMap *m, const void *p, int64_t rows, int64_t stride, int b
            CUDA_SUCCESS;
 }
 
-template <bool SPLIT_P, bool SPLIT>
+template <bool SPLIT_P, Deal DEAL>
 cudaError_t launch_variant(const CUtensorMap &map_q, const CUtensorMap &map_k, const CUtensorMap &map_out, const Args &a, int grid, cudaStream_t st)
 {
     static DeviceOnce once;
@@ -881,15 +954,15 @@ cudaError_t launch_variant(const CUtensorMap &map_q, const CUtensorMap &map_k, c
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess)
         e = once.run(dev, [] {
-            return cudaFuncSetAttribute(prompt_attend_kernel<SPLIT_P, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            return cudaFuncSetAttribute(prompt_attend_kernel<SPLIT_P, DEAL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         (int)SMEM_BYTES);
         });
     if (e != cudaSuccess) return e;
     {
         LaunchScope scope(-1, st);
-        e = launch_pdl(prompt_attend_kernel<SPLIT_P, SPLIT>, dim3(grid), dim3(THREADS), SMEM_BYTES, st, map_q, map_k, map_out, a);
+        e = launch_pdl(prompt_attend_kernel<SPLIT_P, DEAL>, dim3(grid), dim3(THREADS), SMEM_BYTES, st, map_q, map_k, map_out, a);
     }
-    if (e != cudaSuccess || !SPLIT) return e;
+    if (e != cudaSuccess || DEAL != SHARED) return e;
     LaunchScope scope(-1, st);
     return launch_pdl(prompt_join_kernel<SPLIT_P>, dim3(a.tiles * (RT / 4), CHUNKS), dim3(128), 0, st, a, grid);
 }
@@ -914,6 +987,8 @@ cudaError_t launch_prompt_attend(const PromptArgs &p, cudaStream_t st)
     a.heads = p.heads;
     a.window = p.window;
     a.tiles = (int)row_tiles(p.n_q, p.heads);
+    a.lat = p.lat;
+    a.lat_stride = p.lat_stride;
     a.scale = p.scale;
     a.out = p.out;
     a.lse = p.lse;
@@ -924,17 +999,20 @@ cudaError_t launch_prompt_attend(const PromptArgs &p, cudaStream_t st)
     CUtensorMap map_q, map_k, map_out;
     // Without keys the latents' map covers a row of q that every mask leaves out.
     if (!make_map(&map_q, p.q, (int64_t)p.n_q * p.heads, D, RT, 8) ||
-        !make_map(&map_out, p.out, (int64_t)p.n_q * p.heads, D, RT / 2, 1) ||        // f32 outputs do not use it
+        !make_map(&map_out, p.out, (int64_t)p.n_q * p.heads, D, RT, 1) ||        // f32 outputs do not use it
         !make_map(&map_k, p.n_k ? p.lat : p.q, p.n_k ? p.n_k : 1, p.n_k ? p.lat_stride : D, KT, 2))
         return cudaErrorInvalidValue;
-    // Row tiles of one key tile each cannot be shared; many fill the SMs as they are.
-    const bool one = p.n_k <= KT || (p.window > 0 && p.window <= KT && p.heads % RT == 0);
-    if (!one && a.tiles <= MAX_SPLIT_TILES)
-        return p.out_is_fp32 ? launch_variant<true, true>(map_q, map_k, map_out, a, CTAS, st)
-                             : launch_variant<false, true>(map_q, map_k, map_out, a, CTAS, st);
-    const int grid = std::min(a.tiles, CTAS);
-    return p.out_is_fp32 ? launch_variant<true, false>(map_q, map_k, map_out, a, grid, st)
-                         : launch_variant<false, false>(map_q, map_k, map_out, a, grid, st);
+    const bool sliding = p.window > 0 && p.window <= KT && p.heads % RT == 0;
+    if (sliding || p.n_k <= KT || a.tiles > MAX_SPLIT_TILES) {         // one key tile each, or enough for every SM
+        const int grid = std::min(a.tiles, CTAS);
+        if (sliding)
+            return p.out_is_fp32 ? launch_variant<true, SLIDING>(map_q, map_k, map_out, a, grid, st)
+                                 : launch_variant<false, SLIDING>(map_q, map_k, map_out, a, grid, st);
+        return p.out_is_fp32 ? launch_variant<true, WHOLE>(map_q, map_k, map_out, a, grid, st)
+                             : launch_variant<false, WHOLE>(map_q, map_k, map_out, a, grid, st);
+    }
+    return p.out_is_fp32 ? launch_variant<true, SHARED>(map_q, map_k, map_out, a, CTAS, st)
+                         : launch_variant<false, SHARED>(map_q, map_k, map_out, a, CTAS, st);
 }
 
 }  // namespace csa2

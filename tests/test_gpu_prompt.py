@@ -145,7 +145,7 @@ def test_sharp_and_flat_weights():
 
 
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
-@pytest.mark.parametrize("heads,window", [(64, 0), (16, 0), (16, 40), (100, 0)])
+@pytest.mark.parametrize("heads,window", [(64, 0), (16, 0), (16, 40), (100, 0), (64, 40), (64, 128), (128, 7), (64, 1)])
 def test_latents_that_are_not_finite_reach_only_the_queries_that_see_them(value, heads, window):
     new, past = [30, 50, 3], [10, 0, 200]
     kv = [n + p for n, p in zip(new, past)]
@@ -164,6 +164,31 @@ def test_latents_that_are_not_finite_reach_only_the_queries_that_see_them(value,
         assert out[sees].isnan().all() and lse[sees].isnan().all()
     else:
         assert (~out[sees].isfinite()).any(-1).all()
+
+
+@pytest.mark.parametrize("heads", [64, 128])
+@pytest.mark.parametrize("window", [128, 127, 33, 1])
+def test_windows_that_slide(heads, window):
+    # long runs, requests that start anew, continue, have one token, or fewer latents than queries
+    _check_all([400, 1, 1, 290, 5, 129, 700, 0, 128], [0, 0, 500, 31, -3, -129, 128, 9, 1], heads, window, False,
+               seed=window)
+    _check_all([3, 160], [1, 127], heads, window, True, seed=window)
+
+
+@pytest.mark.parametrize("window", [128, 50])
+def test_a_sliding_window_passes_over_latents_that_are_not_finite(window):
+    n = 1500                                   # several tokens a run: bad ones ahead of it, inside it and behind it
+    q, lat = _inputs(window, [n], [n], 64, 0, 4)
+    clean, clean_lse, _ = _call(q, lat, _cu([n]), _cu([n]), window)
+    bad = lat.clone()
+    hit = torch.zeros(n, dtype=torch.bool, device="cuda")
+    for at in (0, 3, 130, 700, 701, 1002, n - 1):
+        bad[at] = float("nan")
+        hit[at:at + window] = True
+    bad[n:] = float("nan")
+    out, lse, _ = _call(q, bad, _cu([n]), _cu([n]), window)
+    assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse[~hit], clean_lse[~hit])
+    assert out[hit].isnan().all() and lse[hit].isnan().all()
 
 
 def test_queries_that_are_not_finite_stay_alone():
