@@ -124,14 +124,23 @@ __device__ __forceinline__ int request_of(const Args &a, int t)
     return b;
 }
 
-// Keys [lo, hi) of token t of request b: within [0, n_k] and hi >= lo however
-// the prefix sums look, non-decreasing in t where they are sound.
-__device__ __forceinline__ void key_range(const Args &a, int b, int t, int &lo, int &hi)
+// A request: its tokens end before q1, its keys are [k0, k1), all clamped to
+// what exists.
+struct Request {
+    int q1, k0, k1;
+};
+__device__ __forceinline__ Request request(const Args &a, int b)
 {
-    const int back = max(1, min(a.n_q, __ldg(a.cu_q + b + 1)) - t);    // this token and those behind it
-    const int k0 = max(0, min(a.n_k, __ldg(a.cu_k + b))), k1 = max(0, min(a.n_k, __ldg(a.cu_k + b + 1)));
-    hi = max(k0, k1 - back + 1);
-    lo = a.window > 0 ? max(k0, hi - a.window) : k0;
+    return {min(a.n_q, __ldg(a.cu_q + b + 1)), max(0, min(a.n_k, __ldg(a.cu_k + b))), max(0, min(a.n_k, __ldg(a.cu_k + b + 1)))};
+}
+
+// Keys [lo, hi) of its token t: within [0, n_k] and hi >= lo however the
+// prefix sums look, non-decreasing in t where they are sound.
+__device__ __forceinline__ void key_range(const Args &a, const Request &q, int t, int &lo, int &hi)
+{
+    const int back = max(1, q.q1 - t);                                 // this token and those behind it
+    hi = max(q.k0, q.k1 - back + 1);
+    lo = a.window > 0 ? max(q.k0, hi - a.window) : q.k0;
 }
 
 // Key tiles of a row tile, 0 if it has no live row; key0 gets the first key
@@ -147,9 +156,10 @@ __device__ __forceinline__ int key_tiles(const Args &a, int live, int tile, int 
     for (int b = request_of(a, t); t <= t1; ++b) {
         if (b < a.batch - 1 && __ldg(a.cu_q + b + 1) <= t) continue;   // an empty request
         const int e = b < a.batch - 1 ? max(t, min(t1, __ldg(a.cu_q + b + 1) - 1)) : t1;
+        const Request q = request(a, b);
         int lo, hi, lo1;
-        key_range(a, b, t, lo, hi);
-        if (e > t) key_range(a, b, e, lo1, hi);
+        key_range(a, q, t, lo, hi);
+        if (e > t) key_range(a, q, e, lo1, hi);
         p = max(p, lo);
         if (hi > p && hi > lo) {
             const int c = (hi - p + KT - 1) / KT;
@@ -231,6 +241,12 @@ __device__ __forceinline__ bool group_any(int group, bool v)
     return r != 0;
 }
 
+// Brings a box to L2 only.
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"((uint64_t)map), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int x, int y, int z)
 {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];\n\t"
@@ -280,6 +296,7 @@ __device__ void producer(const Args &a, Misc *m, uint8_t *sm, const CUtensorMap 
         last = (int)((int64_t)a.tiles * (blockIdx.x + 1) / gridDim.x);
     }
     int64_t left = DEAL == SHARED ? share.units : 0;
+    Request req = {-1, 0, 0};
     int base = 0, top = -1;                                            // SLIDING: the ring holds keys [top - 128, top)
     uint32_t unit = 0;
     for (uint32_t s = 0;; ++s) {
@@ -310,13 +327,22 @@ __device__ void producer(const Args &a, Misc *m, uint8_t *sm, const CUtensorMap 
             g.n = 1;
         }
         int lo[2] = {0, 0}, hi[2] = {-1, -1};                          // hi < 0: no such row
-        if (g.tile >= 0) {
+        if (DEAL == SLIDING && g.tile >= 0) {                          // rows of one token
+            const int t = g.tile * RT / a.heads;
+            if (t >= req.q1) req = request(a, request_of(a, t));       // loads, one after another: once a request
+            key_range(a, req, t, lo[0], hi[0]);
+            if (hi[0] <= lo[0]) lo[0] = hi[0] = 0;                     // no keys
+            lo[1] = g.max_lo = lo[0];
+            hi[1] = g.min_hi = hi[0];
+            g.uniform = hi[0] > 0;
+            g.boxed = true;
+        } else if (g.tile >= 0) {
             int max_lo = 0, min_hi = INT32_MAX, min_lo = INT32_MAX, max_hi = -1;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int t = (g.tile * RT + 32 * i + lane) / a.heads;
                 if (t < live) {
-                    key_range(a, request_of(a, t), t, lo[i], hi[i]);
+                    key_range(a, request(a, request_of(a, t)), t, lo[i], hi[i]);
                     if (hi[i] <= lo[i]) lo[i] = hi[i] = 0;             // no keys
                     max_lo = max(max_lo, lo[i]);
                     min_hi = min(min_hi, hi[i]);
@@ -367,6 +393,8 @@ __device__ void producer(const Args &a, Misc *m, uint8_t *sm, const CUtensorMap 
         if (ok && elect_one()) {
             mbar_arrive_expect_tx(&m->q_full, 8 * Q_SLAB);
             tma_load_3d(sm + Q_OFF, map_q, 0, g.tile * RT, 0, &m->q_full);
+            // the rows after these come to L2 meanwhile: from memory they would arrive after the last product
+            if (DEAL == SLIDING) tma_prefetch_3d(map_q, 0, (g.tile + 1) * RT, 0);
         }
         int key0 = DEAL == SLIDING ? base : g.key0;
         for (int k = 0; ok && k < g.n; ++k, ++unit, key0 = next_tile(g, m->lo[r], m->hi[r], key0)) {
@@ -404,6 +432,7 @@ __device__ void producer(const Args &a, Misc *m, uint8_t *sm, const CUtensorMap 
     }
 }
 
+// Issues every product.
 template <bool SPLIT_P>
 __device__ void mma_issuer(Misc *m, uint8_t *sm)
 {
@@ -412,13 +441,18 @@ __device__ void mma_issuer(Misc *m, uint8_t *sm)
     const uint64_t k_chans = smem_desc(smem_addr(sm + K_OFF), K_SLAB, 1024), p_rows = smem_desc(smem_addr(sm + P_OFF), 8192, 1024);
     const uint32_t tb = m->tmem;
     uint32_t unit = 0;
-    for (uint32_t s = 0;; ++s) {
-        const uint32_t r = s & 1;
-        if (!wait(m, &m->seg_full[r], (s >> 1) & 1)) return;
-        const int n = m->seg[r].n;
-        mbar_arrive(&m->seg_empty[r]);
-        if (n == 0) return;
+    // The next segment is looked up before the last product of this one, so
+    // that nothing stands between that product and the next S.
+    auto length = [&](uint32_t s) {
+        if (!wait(m, &m->seg_full[s & 1], (s >> 1) & 1)) return 0;
+        const int n = m->seg[s & 1].n;
+        mbar_arrive(&m->seg_empty[s & 1]);
+        return n;
+    };
+    int n = length(0);
+    for (uint32_t s = 0; n > 0; ++s) {
         if (!wait(m, &m->q_full, s & 1)) return;
+        int next = 0;
         for (int k = 0; k < n; ++k, ++unit) {
 #pragma unroll
             for (int c = 0; c < CHUNKS; ++c) {
@@ -429,9 +463,12 @@ __device__ void mma_issuer(Misc *m, uint8_t *sm)
                            q_rows + ((2 * c + (i >> 2)) * Q_SLAB + (i & 3) * 32) / 16, IDESC_S, (c > 0 || i > 0) ? 1u : 0u);
             }
             mma_commit(&m->s_full);
-            if (k == n - 1) mma_commit(&m->q_empty);
-            if (!wait(m, &m->p_full, unit & 1)) return;
+            if (k == n - 1) {
+                mma_commit(&m->q_empty);
+                next = length(s + 1);
+            }
             if (k == 0 && !wait(m, &m->o_empty, (s & 1) ^ 1)) return;  // the last row tile's output is out of O
+            if (!wait(m, &m->p_full, unit & 1)) return;
             fence_after_sync();
 #pragma unroll
             for (int c = 0; c < CHUNKS; ++c) {
@@ -443,6 +480,7 @@ __device__ void mma_issuer(Misc *m, uint8_t *sm)
             }
             if (k == n - 1) mma_commit(&m->o_full);
         }
+        n = next;
     }
 }
 
@@ -853,14 +891,16 @@ prompt_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     }
 }
 
-// Joins the parts of the row tiles that several CTAs of `grid` shared; four rows per CTA.
+// Joins the parts of the row tiles that several CTAs of `grid` shared.  A CTA
+// takes four rows x 128 channels; blockDim.y groups of threads share the parts.
+constexpr int JOIN_GROUPS = 8;
 template <bool F32>
-__global__ void __launch_bounds__(128) prompt_join_kernel(const Args a, int grid)
+__global__ void __launch_bounds__(128 * JOIN_GROUPS) prompt_join_kernel(const Args a, int grid)
 {
     grid_dependency_wait();
     allow_dependents();
     const int tile = blockIdx.x / (RT / 4), i = 4 * (blockIdx.x % (RT / 4));
-    const int c = blockIdx.y, d = 128 * c + threadIdx.x;
+    const int c = blockIdx.y, d = 128 * c + threadIdx.x, group = threadIdx.y, groups = blockDim.y;
     const int64_t total = a.prefix[a.tiles], u0 = a.prefix[tile], u1 = a.prefix[tile + 1];
     const int64_t row = (int64_t)tile * RT + i, live = (int64_t)live_tokens(a) * a.heads;
     if (u1 == u0 || row >= live) return;
@@ -872,8 +912,9 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const Args a, int grid
     const size_t first = 2 * (size_t)c0 + (total * c0 / ctas >= u0 ? 0 : 1);
     const int n = c1 - c0 + 1;
     __shared__ float weight[4][CTAS], inv[4];
+    __shared__ float4 sums[JOIN_GROUPS][128];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    {                                                                  // warp w: weights of row i + w
+    if (group == 0) {                                                  // warp w: weights of row i + w
         float top = -INFINITY, sum = 0.0f;
         for (int k = lane; k < n; k += 32)
             top = fmaxf(top, a.part_ml[(k ? 2 * (size_t)(c0 + k) : first) * RT + i + warp].x);
@@ -894,21 +935,34 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const Args a, int grid
         }
     }
     __syncthreads();
-    float o[4] = {0.f, 0.f, 0.f, 0.f};
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-    for (int k = 0; k < n; ++k) {
+    for (int k = group; k < n; k += groups) {
         const float4 v = *reinterpret_cast<const float4 *>(a.part_o + (k ? 2 * (size_t)(c0 + k) : first) * RT * D + part_at(i, d));
-        o[0] += weight[0][k] * v.x;
-        o[1] += weight[1][k] * v.y;
-        o[2] += weight[2][k] * v.z;
-        o[3] += weight[3][k] * v.w;
+        o.x += weight[0][k] * v.x;
+        o.y += weight[1][k] * v.y;
+        o.z += weight[2][k] * v.z;
+        o.w += weight[3][k] * v.w;
     }
+    if (groups > 1) {
+        sums[group][threadIdx.x] = o;
+        __syncthreads();
+        if (group > 0) return;
+        for (int k = 1; k < groups; ++k) {                             // in order: the same result every time
+            const float4 v = sums[k][threadIdx.x];
+            o.x += v.x;
+            o.y += v.y;
+            o.z += v.z;
+            o.w += v.w;
+        }
+    }
+    const float v[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         if (row + j >= live) break;
         const size_t at = (size_t)(row + j) * D + d;
-        if (F32) ((float *)a.out)[at] = o[j] * inv[j];
-        else ((__nv_bfloat16 *)a.out)[at] = __float2bfloat16_rn(o[j] * inv[j]);
+        if (F32) ((float *)a.out)[at] = v[j] * inv[j];
+        else ((__nv_bfloat16 *)a.out)[at] = __float2bfloat16_rn(v[j] * inv[j]);
     }
 }
 
@@ -964,7 +1018,9 @@ cudaError_t launch_variant(const CUtensorMap &map_q, const CUtensorMap &map_k, c
     }
     if (e != cudaSuccess || DEAL != SHARED) return e;
     LaunchScope scope(-1, st);
-    return launch_pdl(prompt_join_kernel<SPLIT_P>, dim3(a.tiles * (RT / 4), CHUNKS), dim3(128), 0, st, a, grid);
+    // about 8 parts to a group of threads, if every SM works on the same few row tiles
+    const int groups = std::max(1, std::min(JOIN_GROUPS, grid / (8 * a.tiles)));
+    return launch_pdl(prompt_join_kernel<SPLIT_P>, dim3(a.tiles * (RT / 4), CHUNKS), dim3(128, groups), 0, st, a, grid);
 }
 
 }  // namespace
