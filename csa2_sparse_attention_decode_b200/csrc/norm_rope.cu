@@ -10,8 +10,10 @@
 // the fp32 sine: at position 2^20 an fp32 product is off by up to 0.06 rad.
 //
 // Bound: 4 bytes per element, read and written once.  A row stays in its
-// warp's registers (16 bytes a lane and load), so there is nothing to re-read;
-// a CTA computes a token's sines once, in shared memory, for all its heads.
+// warp's registers, so nothing is read twice.  A warp has 2 KB of rows in
+// flight (two rows of 512 channels, four of 256, ...), takes a slice of a
+// token's rows with their weights in registers, and forms the token's sines
+// once for the slice, in its own shared memory.
 #include "common.cuh"
 #include "serve.cuh"
 
@@ -19,7 +21,7 @@ namespace csa2 {
 namespace {
 
 constexpr int THREADS = 256;
-constexpr int MAX_TOKENS = 8;                  // tokens of one CTA
+constexpr int WARPS = THREADS / 32;
 
 __device__ __forceinline__ void unpack8(const uint4 &v, float (&x)[8])
 {
@@ -37,154 +39,177 @@ __device__ __forceinline__ uint32_t pack2(float a, float b)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// DIM channels a row; UNROLL rows in flight per lane group.  A CTA takes
-// `tokens` consecutive tokens and, of their rows, [y * rows_per_cta, ...).
-template <int DIM, int UNROLL>
-__global__ void __launch_bounds__(THREADS) norm_rope_kernel(NormRopeArgs a, int tokens, int rows_per_cta)
+// DIM channels a row.  A step is 1 KB of rows: a lane holds two 16-byte chunks
+// of one row.  With halves its second chunk is the first one's partner, `away`
+// chunks on, so that the rotation stays in the lane.
+template <int DIM>
+struct Shape {
+    static constexpr int CHUNKS = DIM / 8;                             // of a row
+    static constexpr int LANES = CHUNKS / 2;                           // of a row
+    static constexpr int ROWS = 32 / LANES;                            // of a step
+};
+
+// The cosine and sine of pair p lie so that lanes with neighbouring chunks read
+// neighbouring 16 bytes: two pairs in each, `per` pairs to a chunk.
+__device__ __forceinline__ int turn_at(int p, int per, int half) { return ((p % per / 2) * (half / per) + p / per) * 2 + (p & 1); }
+
+// A warp forms a token's cosines and sines.  Not inlined: its registers would
+// crowd out the rows in flight.
+__device__ __noinline__ void fill_turns(float2 *turn, const float *inv_freq, int half, int per, int pos, float sign)
 {
-    constexpr int CHUNKS = DIM / 8;                                    // 16-byte chunks of a row
-    constexpr int LANES = CHUNKS < 32 ? CHUNKS : 32;                   // lanes of a row
-    constexpr int CPL = CHUNKS / LANES;                                // chunks a lane
-    constexpr int GROUPS = THREADS / LANES;                            // rows in a pass of the CTA
-    extern __shared__ float2 turn[];                                   // [tokens][R/2] cosine, sine
-    const int l = threadIdx.x & (LANES - 1), g = threadIdx.x / LANES;
-    const int half = a.rot_dim / 2;
-    grid_dependency_wait();
-    allow_dependents();
-
-    const int n = a.n_valid ? max(0, min(a.n, *a.n_valid)) : a.n;
-    const int t0 = blockIdx.x * tokens, nt = min(tokens, n - t0);
-    if (nt <= 0) return;
-    const int per_token = a.heads + a.kv_heads;
-    const int r0 = blockIdx.y * rows_per_cta, r1 = min(nt * per_token, r0 + rows_per_cta);
-
-    for (int i = threadIdx.x; i < nt * half; i += THREADS) {
-        const int t = i / half;
-        double x = (double)a.pos[t0 + t] * (double)a.inv_freq[i - t * half] * 0.15915494309189535;   // 1 / 2 pi
-        x -= rint(x);
-        float s, c;
-        sincospif(2.0f * (float)x, &s, &c);
-        if (a.flags & CSA2_ROPE_INVERSE) s = -s;
-        turn[i] = make_float2(c, s);
+    for (int i = threadIdx.x & 31; i < half; i += 32) {
+        double t = (double)pos * (double)inv_freq[i] * 0.15915494309189535;            // 1 / 2 pi
+        t -= rint(t);
+        float sine, cosine;
+        sincospif(2.0f * (float)t, &sine, &cosine);
+        turn[turn_at(i, per, half)] = make_float2(cosine, sign * sine);
     }
-    __syncthreads();
+}
 
-    for (int rb = r0 + g * UNROLL; rb - g * UNROLL < r1; rb += GROUPS * UNROLL) {   // uniform in a warp: shuffles below
-        uint4 raw[UNROLL][CPL];
+// Norm and rotation of one step: x holds chunks c[0] and c[1] of a row, w the weights there.
+template <int DIM>
+__device__ __forceinline__ void finish(const NormRopeArgs &a, const uint4 (&raw)[2], float (&x)[2][8], const float (&w)[2][8],
+                                       const float4 *turn, const int (&c)[2])
+{
+    unpack8(raw[0], x[0]);
+    unpack8(raw[1], x[1]);
+    if (!(a.flags & CSA2_ROPE_NO_NORM)) {
+        float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-            const int r = rb + u;
-            if (r < r1) {
-                const int t = r / per_token, h = r - t * per_token;
-                const uint16_t *src = h < a.heads ? a.q + (int64_t)(t0 + t) * a.q_stride + (int64_t)h * DIM
-                                                  : a.k + (int64_t)(t0 + t) * a.k_stride + (int64_t)(h - a.heads) * DIM;
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int j = 0; j < CPL; ++j) raw[u][j] = *reinterpret_cast<const uint4 *>(src + 8 * (l + j * LANES));
-            } else {
+            for (int i = 0; i < 8; ++i) sum[k] += x[k][i] * x[k][i];
+        sum[0] += sum[1];
 #pragma unroll
-                for (int j = 0; j < CPL; ++j) raw[u][j] = make_uint4(0, 0, 0, 0);
+        for (int d = Shape<DIM>::LANES / 2; d > 0; d >>= 1) sum[0] += __shfl_xor_sync(~0u, sum[0], d);
+        const float inv = rsqrtf(sum[0] * (1.0f / DIM) + a.eps);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[k][i] = x[k][i] * inv * w[k][i];
+    }
+    if (a.rot_dim == 0) return;
+    const int skip = (DIM - a.rot_dim) / 8;                            // chunks before the rotated range
+    if (!(a.flags & CSA2_ROPE_HALVES)) {
+        const int chunks = a.rot_dim / 8;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (c[k] < skip) continue;
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+                const float4 v = turn[i / 2 * chunks + c[k] - skip];
+                const float a0 = x[k][2 * i], b0 = x[k][2 * i + 1], a1 = x[k][2 * i + 2], b1 = x[k][2 * i + 3];
+                x[k][2 * i] = a0 * v.x - b0 * v.y;
+                x[k][2 * i + 1] = a0 * v.y + b0 * v.x;
+                x[k][2 * i + 2] = a1 * v.z - b1 * v.w;
+                x[k][2 * i + 3] = a1 * v.w + b1 * v.z;
             }
         }
+    } else if (c[0] >= skip) {
+        const int chunks = a.rot_dim / 16;
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-            const int r = rb + u;
-            const int t = r / per_token, h = r - t * per_token;
-            const bool is_q = h < a.heads;
-            float x[CPL][8], sum = 0.0f;
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) {
-                unpack8(raw[u][j], x[j]);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sum += x[j][i] * x[j][i];
-            }
-            if (!(a.flags & CSA2_ROPE_NO_NORM)) {
-#pragma unroll
-                for (int d = LANES / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
-                const float inv = rsqrtf(sum * (1.0f / DIM) + a.eps);
-                const float *w = is_q ? a.q_weight : a.k_weight;
-#pragma unroll
-                for (int j = 0; j < CPL; ++j) {
-                    const float4 *wp = reinterpret_cast<const float4 *>(w + 8 * (l + j * LANES));
-                    const float4 wa = wp[0], wb = wp[1];
-                    const float ww[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[j][i] = x[j][i] * inv * ww[i];
-                }
-            }
-            if (half) {
-                const float2 *cs = turn + min(t, nt - 1) * half;
-                if (!(a.flags & CSA2_ROPE_HALVES)) {
-#pragma unroll
-                    for (int j = 0; j < CPL; ++j) {
-                        const int p0 = (8 * (l + j * LANES) - (DIM - a.rot_dim)) / 2;      // the chunk's first pair
-                        if (8 * (l + j * LANES) >= DIM - a.rot_dim) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float2 v = cs[p0 + i];
-                                const float xa = x[j][2 * i], xb = x[j][2 * i + 1];
-                                x[j][2 * i] = xa * v.x - xb * v.y;
-                                x[j][2 * i + 1] = xa * v.y + xb * v.x;
-                            }
-                        }
-                    }
-                } else {
-                    // The rotated range starts at a multiple of its own length,
-                    // so a chunk's partner is half / 8 chunks away by exclusive or.
-                    const int away = half / 8;
-                    float y[CPL][8];
-#pragma unroll
-                    for (int j = 0; j < CPL; ++j)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            y[j][i] = away < LANES ? __shfl_xor_sync(~0u, x[j][i], away) : x[CPL - 1 - j][i];
-#pragma unroll
-                    for (int j = 0; j < CPL; ++j) {
-                        const int c0 = 8 * (l + j * LANES) - (DIM - a.rot_dim);
-                        if (c0 >= 0) {
-                            const bool upper = c0 >= half;
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float2 v = cs[(upper ? c0 - half : c0) + i];
-                                x[j][i] = upper ? y[j][i] * v.y + x[j][i] * v.x : x[j][i] * v.x - y[j][i] * v.y;
-                            }
-                        }
-                    }
-                }
-            }
-            if (r >= r1) continue;
-            const int64_t row = is_q ? (int64_t)(t0 + t) * a.heads + h : (int64_t)(t0 + t) * a.kv_heads + (h - a.heads);
-            uint16_t *dst = is_q ? a.q_out : a.k_out;
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) {
-                const int64_t at = row * DIM + 8 * (l + j * LANES);
-                if (dst)
-                    *reinterpret_cast<uint4 *>(dst + at) =
-                        make_uint4(pack2(x[j][0], x[j][1]), pack2(x[j][2], x[j][3]), pack2(x[j][4], x[j][5]),
-                                   pack2(x[j][6], x[j][7]));
-                if (!is_q && a.k_out_f32) {
-                    float4 *f = reinterpret_cast<float4 *>(a.k_out_f32 + at);
-                    f[0] = make_float4(x[j][0], x[j][1], x[j][2], x[j][3]);
-                    f[1] = make_float4(x[j][4], x[j][5], x[j][6], x[j][7]);
-                }
-            }
+        for (int i = 0; i < 8; i += 2) {
+            const float4 v = turn[i / 2 * chunks + c[0] - skip];
+            const float a0 = x[0][i], b0 = x[1][i], a1 = x[0][i + 1], b1 = x[1][i + 1];
+            x[0][i] = a0 * v.x - b0 * v.y;
+            x[1][i] = a0 * v.y + b0 * v.x;
+            x[0][i + 1] = a1 * v.z - b1 * v.w;
+            x[1][i + 1] = a1 * v.w + b1 * v.z;
         }
     }
 }
 
-template <int DIM, int UNROLL>
+// `slices` warps share a token; a warp takes every slices-th of its steps,
+// queries first, then latents.
+template <int DIM>
+__global__ void __launch_bounds__(THREADS, 4) norm_rope_kernel(NormRopeArgs a, int slices, int q_steps, int steps)
+{
+    using S = Shape<DIM>;
+    extern __shared__ __align__(16) float2 turns[];                    // [WARPS][R/2] cosine, sine
+    const int lane = threadIdx.x & 31, l = lane & (S::LANES - 1), sub = lane / S::LANES;
+    const int half = a.rot_dim / 2, per = a.flags & CSA2_ROPE_HALVES ? 8 : 4;
+    const int away = a.flags & CSA2_ROPE_HALVES && half ? half / 8 : S::LANES;
+    const int c[2] = {(l / away * 2) * away + l % away, (l / away * 2 + 1) * away + l % away};
+    float2 *turn = turns + (threadIdx.x >> 5) * half;
+    grid_dependency_wait();
+    allow_dependents();
+
+    const int n = a.n_valid ? max(0, min(a.n, *a.n_valid)) : a.n;
+    const int64_t items = (int64_t)n * slices;
+    float w[2][8] = {};
+    int weights_of = -1;                                               // 1: of the queries, 0: of the latents
+    for (int64_t item = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5); item < items; item += (int64_t)gridDim.x * WARPS) {
+        const int token = (int)(item / slices), slice = (int)(item - (int64_t)token * slices);
+        bool turned = half == 0;
+        for (int step = slice; step < steps;) {
+            const bool is_q = step < q_steps;
+            const int heads = is_q ? a.heads : a.kv_heads, end = is_q ? q_steps : steps;
+            // the lane's row of this step and of the slice's next
+            const int h[2] = {(is_q ? step : step - q_steps) * S::ROWS + sub, (is_q ? step : step - q_steps) * S::ROWS + sub + slices * S::ROWS};
+            const bool two = step + slices < end;
+            const bool live[2] = {h[0] < heads, two && h[1] < heads};
+            const uint16_t *src = is_q ? a.q + (int64_t)token * a.q_stride : a.k + (int64_t)token * a.k_stride;
+            uint4 raw[2][2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    raw[u][k] = live[u] ? *reinterpret_cast<const uint4 *>(src + h[u] * DIM + 8 * c[k]) : make_uint4(0, 0, 0, 0);
+            if (weights_of != (int)is_q && !(a.flags & CSA2_ROPE_NO_NORM)) {
+                weights_of = is_q;
+                const float *ws = is_q ? a.q_weight : a.k_weight;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float4 wa = *reinterpret_cast<const float4 *>(ws + 8 * c[k]), wb = *reinterpret_cast<const float4 *>(ws + 8 * c[k] + 4);
+                    w[k][0] = wa.x, w[k][1] = wa.y, w[k][2] = wa.z, w[k][3] = wa.w;
+                    w[k][4] = wb.x, w[k][5] = wb.y, w[k][6] = wb.z, w[k][7] = wb.w;
+                }
+            }
+            if (!turned) {                                             // while the rows are on their way
+                turned = true;
+                __syncwarp();
+                fill_turns(turn, a.inv_freq, half, per, a.pos[token], a.flags & CSA2_ROPE_INVERSE ? -1.0f : 1.0f);
+                __syncwarp();
+            }
+            uint16_t *dst = is_q ? a.q_out : a.k_out;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (u == 1 && !two) break;
+                float x[2][8];
+                finish<DIM>(a, raw[u], x, w, reinterpret_cast<const float4 *>(turn), c);
+                if (!live[u]) continue;
+                const int64_t to = ((int64_t)token * heads + h[u]) * DIM;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    if (dst)
+                        *reinterpret_cast<uint4 *>(dst + to + 8 * c[k]) = make_uint4(
+                            pack2(x[k][0], x[k][1]), pack2(x[k][2], x[k][3]), pack2(x[k][4], x[k][5]), pack2(x[k][6], x[k][7]));
+                    if (!is_q && a.k_out_f32) {
+                        float4 *f = reinterpret_cast<float4 *>(a.k_out_f32 + to + 8 * c[k]);
+                        f[0] = make_float4(x[k][0], x[k][1], x[k][2], x[k][3]);
+                        f[1] = make_float4(x[k][4], x[k][5], x[k][6], x[k][7]);
+                    }
+                }
+            }
+            step += two ? 2 * slices : slices;
+        }
+    }
+}
+
+template <int DIM>
 cudaError_t launch_dim(const NormRopeArgs &a, cudaStream_t st)
 {
-    constexpr int GROUPS = THREADS / (DIM / 8 < 32 ? DIM / 8 : 32);
-    const int per_token = a.heads + a.kv_heads;
-    // Enough rows a CTA to pay for its start, few enough to fill 148 SMs.
-    int tokens = std::max(1, std::min(MAX_TOKENS, 65536 / (per_token * DIM * 2)));
-    tokens = std::max(1, std::min(tokens, a.n / (2 * 148)));
-    int split = 1;
-    if (a.n < 2 * 148) split = std::max(1, std::min(2 * 148 / a.n, (per_token + GROUPS - 1) / GROUPS));
-    const int rows = (tokens * per_token + split - 1) / split;
+    constexpr int SMS = 148, RESIDENT = 4 * WARPS * SMS;               // warps at once
+    constexpr int ROWS = Shape<DIM>::ROWS;
+    const int q_steps = (a.heads + ROWS - 1) / ROWS, steps = q_steps + (a.kv_heads + ROWS - 1) / ROWS;
+    // A warp forms the sines for its slice of a token: 8 steps pay for them.
+    // Fewer tokens than warps: down to one pass of two steps each.
+    int slices = std::max(1, steps / 8);
+    if ((int64_t)a.n * slices < RESIDENT) slices = std::max(slices, std::min((steps + 1) / 2, RESIDENT / a.n));
+    const int64_t blocks = ((int64_t)a.n * slices + WARPS - 1) / WARPS;
     LaunchScope scope(-1, st);
-    return launch_pdl(norm_rope_kernel<DIM, UNROLL>, dim3((a.n + tokens - 1) / tokens, split), dim3(THREADS),
-                      sizeof(float2) * tokens * (a.rot_dim / 2), st, a, tokens, rows);
+    return launch_pdl(norm_rope_kernel<DIM>, dim3((unsigned)std::min<int64_t>(blocks, RESIDENT / WARPS)), dim3(THREADS),
+                      sizeof(float2) * WARPS * (a.rot_dim / 2), st, a, slices, q_steps, steps);
 }
 
 }  // namespace
@@ -192,10 +217,10 @@ cudaError_t launch_dim(const NormRopeArgs &a, cudaStream_t st)
 cudaError_t launch_norm_rope(const NormRopeArgs &a, int dim, cudaStream_t st)
 {
     switch (dim) {
-    case 64: return launch_dim<64, 2>(a, st);
-    case 128: return launch_dim<128, 2>(a, st);
-    case 256: return launch_dim<256, 2>(a, st);
-    case 512: return launch_dim<512, 2>(a, st);
+    case 64: return launch_dim<64>(a, st);
+    case 128: return launch_dim<128>(a, st);
+    case 256: return launch_dim<256>(a, st);
+    case 512: return launch_dim<512>(a, st);
     }
     return cudaErrorInvalidValue;
 }
