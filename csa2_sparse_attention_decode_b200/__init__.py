@@ -116,7 +116,13 @@ def _ptr(t):
     return C.c_void_p(t.data_ptr())
 
 
+# The current stream's handle without building a Stream object (3 us of a call's host time).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
+    if stream is None and _raw_stream is not None:
+        return C.c_void_p(_raw_stream(torch.cuda.current_device()))
     s = torch.cuda.current_stream() if stream is None else stream
     return C.c_void_p(s.cuda_stream)
 
@@ -321,23 +327,29 @@ def csa2_selftest_wait_timeout(error_word, polls: int = 1024, stream=None):
 
 
 # ---------------------------------------------------------------- around the layers
-def _typed(name, t, dtype, shape):
-    """The device pointer of t after its device, type and shape are checked (None passes)."""
+def _typed(name, t, dtype, shape, dev):
+    """The device pointer of t after its type, shape and device are checked (None passes)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape:
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name}: {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError("libcsa2 takes contiguous tensors")
-    return _here(t)
+    return _here(t, dev)
 
 
-def _here(t):
+def _here(t, dev):
     if not t.is_cuda:
         raise ValueError("libcsa2 takes device tensors")
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise ValueError("libcsa2 takes tensors of the current device")
     return t.data_ptr()
+
+
+def _device():
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2      # -1 is the host
 
 
 def csa2_verify(target, probs, draft, n_draft, u, n_accepted, tokens, error, stream=None):
@@ -347,12 +359,12 @@ def csa2_verify(target, probs, draft, n_draft, u, n_accepted, tokens, error, str
     [batch] and tokens [batch, k+1] (kept drafts, drawn token, -1) receive the
     outcome."""
     B, k1, V = (int(x) for x in target.shape)
-    f32, i32 = torch.float32, torch.int32
+    f32, i32, dev = torch.float32, torch.int32, _device()
     _check("csa2_verify", lib.csa2_verify(
-        B, k1 - 1, V, _typed("target", target, f32, (B, k1, V)), _typed("probs", probs, f32, (B, k1 - 1, V)),
-        _typed("draft", draft, i32, (B, k1 - 1)), _typed("n_draft", n_draft, i32, (B,)),
-        _typed("u", u, f32, (B, k1)), _typed("n_accepted", n_accepted, i32, (B,)),
-        _typed("tokens", tokens, i32, (B, k1)), _typed("error", error, i32, (1,)), _stream(stream)))
+        B, k1 - 1, V, _typed("target", target, f32, (B, k1, V), dev), _typed("probs", probs, f32, (B, k1 - 1, V), dev),
+        _typed("draft", draft, i32, (B, k1 - 1), dev), _typed("n_draft", n_draft, i32, (B,), dev),
+        _typed("u", u, f32, (B, k1), dev), _typed("n_accepted", n_accepted, i32, (B,), dev),
+        _typed("tokens", tokens, i32, (B, k1), dev), _typed("error", error, i32, (1,), dev), _stream(stream)))
 
 
 def csa2_plan_tokens(n_tokens, n_new, m, page_table, free_pages, n_free, n_free_out, cu_new, token_req, token_pos,
@@ -362,17 +374,17 @@ def csa2_plan_tokens(n_tokens, n_new, m, page_table, free_pages, n_free, n_free_
     [n_pages] are updated; n_free, n_free_out [1]; cu_new [batch+1];
     token_req, token_pos, token_slot [max_new]."""
     B, width = (int(x) for x in page_table.shape)
-    n_pages, room, i32 = int(free_pages.shape[0]), int(token_req.shape[0]), torch.int32
+    n_pages, room, i32, dev = int(free_pages.shape[0]), int(token_req.shape[0]), torch.int32, _device()
     _check("csa2_plan_tokens", lib.csa2_plan_tokens(
-        B, width, n_pages, room, _typed("n_tokens", n_tokens, i32, (B,)), _typed("n_new", n_new, i32, (B,)),
-        _typed("m", m, i32, (B,)), _typed("page_table", page_table, i32, (B, width)),
-        _typed("free_pages", free_pages, i32, (n_pages,)), _typed("n_free", n_free, i32, (1,)),
-        _typed("n_free_out", n_free_out, i32, (1,)), _typed("cu_new", cu_new, i32, (B + 1,)),
-        _typed("token_req", token_req, i32, (room,)), _typed("token_pos", token_pos, i32, (room,)),
-        _typed("token_slot", token_slot, i32, (room,)), _typed("error", error, i32, (1,)), _stream(stream)))
+        B, width, n_pages, room, _typed("n_tokens", n_tokens, i32, (B,), dev), _typed("n_new", n_new, i32, (B,), dev),
+        _typed("m", m, i32, (B,), dev), _typed("page_table", page_table, i32, (B, width), dev),
+        _typed("free_pages", free_pages, i32, (n_pages,), dev), _typed("n_free", n_free, i32, (1,), dev),
+        _typed("n_free_out", n_free_out, i32, (1,), dev), _typed("cu_new", cu_new, i32, (B + 1,), dev),
+        _typed("token_req", token_req, i32, (room,), dev), _typed("token_pos", token_pos, i32, (room,), dev),
+        _typed("token_slot", token_slot, i32, (room,), dev), _typed("error", error, i32, (1,), dev), _stream(stream)))
 
 
-def _heads(name, t):
+def _heads(name, t, dev):
     """(pointer, heads, dim, token stride) of a bf16 [n, heads, dim] tensor whose
     tokens may lie apart (a slice of a wider projection); None has no heads."""
     if t is None:
@@ -382,7 +394,7 @@ def _heads(name, t):
     n, h, d = (int(x) for x in t.shape)
     if t.numel() and (t.stride(2) != 1 or (h > 1 and t.stride(1) != d)):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return _here(t), h, d, t.stride(0) if n > 1 else h * d
+    return _here(t, dev), h, d, t.stride(0) if n > 1 else h * d
 
 
 def csa2_norm_rope(q, k, pos, inv_freq, q_weight, k_weight, eps: float, q_out, k_out, k_out_f32=None, n_valid=None,
@@ -394,19 +406,20 @@ def csa2_norm_rope(q, k, pos, inv_freq, q_weight, k_weight, eps: float, q_out, k
     ROPE_HALVES | ROPE_INVERSE | ROPE_NO_NORM."""
     if q is None and k is None:
         raise ValueError("csa2_norm_rope needs q or k")
-    qp, h, dq, qs = _heads("q", q)
-    kp, g, dk, ks = _heads("k", k)
+    dev = _device()
+    qp, h, dq, qs = _heads("q", q, dev)
+    kp, g, dk, ks = _heads("k", k, dev)
     n, d = int((q if q is not None else k).shape[0]), dq or dk
     if q is not None and k is not None and (dq != dk or int(k.shape[0]) != n):
         raise ValueError("q and k differ in tokens or channels")
     f32, i32, b16 = torch.float32, torch.int32, torch.bfloat16
     rot = 0 if inv_freq is None else 2 * int(inv_freq.shape[0])
     _check("csa2_norm_rope", lib.csa2_norm_rope(
-        n, d, h, qp, qs, _typed("q_weight", q_weight, f32, (d,)), _typed("q_out", q_out, b16, (n, h, d)), g, kp, ks,
-        _typed("k_weight", k_weight, f32, (d,)), _typed("k_out", k_out, b16, (n, g, d)),
-        _typed("k_out_f32", k_out_f32, f32, (n, g, d)), _typed("pos", pos, i32, (n,)),
-        _typed("inv_freq", inv_freq, f32, (rot // 2,)), rot, float(eps), int(flags),
-        _typed("n_valid", n_valid, i32, (1,)), _stream(stream)))
+        n, d, h, qp, qs, _typed("q_weight", q_weight, f32, (d,), dev), _typed("q_out", q_out, b16, (n, h, d), dev), g, kp, ks,
+        _typed("k_weight", k_weight, f32, (d,), dev), _typed("k_out", k_out, b16, (n, g, d), dev),
+        _typed("k_out_f32", k_out_f32, f32, (n, g, d), dev), _typed("pos", pos, i32, (n,), dev),
+        _typed("inv_freq", inv_freq, f32, (rot // 2,), dev), rot, float(eps), int(flags),
+        _typed("n_valid", n_valid, i32, (1,), dev), _stream(stream)))
 
 
 def csa2_prompt_workspace_bytes(n_q: int, heads: int, n_k: int) -> int:
@@ -420,14 +433,14 @@ def csa2_prompt_attend(q, lat, cu_q, cu_k, window: int, scale: float, out, lse, 
     everything.  out like q, bf16 or f32; lse [n_q, heads] f32 or None; ws:
     uint8, csa2_prompt_workspace_bytes(n_q, heads, n_k)."""
     n_q, heads = int(q.shape[0]), int(q.shape[1])
-    i32, b16 = torch.int32, torch.bfloat16
+    i32, b16, dev = torch.int32, torch.bfloat16, _device()
     if lat.dtype != b16 or lat.dim() != 2 or lat.shape[1] != LATENT or (lat.numel() and lat.stride(1) != 1):
         raise ValueError(f"lat: rows of {LATENT} bfloat16 expected, got {lat.dtype} {tuple(lat.shape)}")
     n_k, batch = int(lat.shape[0]), int(cu_q.shape[0]) - 1
     fp32 = out.dtype == torch.float32
     _check("csa2_prompt_attend", lib.csa2_prompt_attend(
-        batch, _typed("cu_q", cu_q, i32, (batch + 1,)), _typed("cu_k", cu_k, i32, (batch + 1,)), n_q, n_k, heads,
-        _typed("q", q, b16, (n_q, heads, LATENT)), _here(lat), lat.stride(0) if n_k > 1 else LATENT, int(window),
-        float(scale), _typed("out", out, torch.float32 if fp32 else b16, (n_q, heads, LATENT)), int(fp32),
-        _typed("lse", lse, torch.float32, (n_q, heads)), _typed("error", error, i32, (1,)),
-        _typed("ws", ws, torch.uint8, (ws.numel(),)), ws.numel(), _stream(stream)))
+        batch, _typed("cu_q", cu_q, i32, (batch + 1,), dev), _typed("cu_k", cu_k, i32, (batch + 1,), dev), n_q, n_k, heads,
+        _typed("q", q, b16, (n_q, heads, LATENT), dev), _here(lat, dev), lat.stride(0) if n_k > 1 else LATENT, int(window),
+        float(scale), _typed("out", out, torch.float32 if fp32 else b16, (n_q, heads, LATENT), dev), int(fp32),
+        _typed("lse", lse, torch.float32, (n_q, heads), dev), _typed("error", error, i32, (1,), dev),
+        _typed("ws", ws, torch.uint8, (ws.numel(),), dev), ws.numel(), _stream(stream)))

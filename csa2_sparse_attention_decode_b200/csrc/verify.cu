@@ -24,7 +24,7 @@ namespace {
 constexpr int THREADS = 512;
 constexpr int WARPS = THREADS / 32;
 constexpr int MAX_CLUSTER = 8;
-constexpr int UNROLL = 8;
+constexpr int BLOCK = 16;                      // loads of each row in flight, a lane; a block is 16 x 32 weights
 
 __device__ __forceinline__ double warp_sum(double v)
 {
@@ -47,10 +47,71 @@ struct Weights {
     __device__ __forceinline__ double operator()(int v) const { return of(p[v], residual ? draft(v) : 0.0f); }
 };
 
-__global__ void __launch_bounds__(THREADS) verify_kernel(VerifyArgs a)
+// Lanes i and i + 16 get the sum of the warp's i-th values.
+__device__ __forceinline__ double group_sums(double (&v)[BLOCK])
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < BLOCK; ++i) v[i] += __shfl_xor_sync(~0u, v[i], 16);
+#pragma unroll
+    for (int d = BLOCK / 2; d > 0; d >>= 1) {
+        const bool up = lane & d;
+#pragma unroll
+        for (int i = 0; i < d; ++i) {
+            const double keep = up ? v[i + d] : v[i], send = up ? v[i] : v[i + d];
+            v[i] = keep + __shfl_xor_sync(~0u, send, d);
+        }
+    }
+    return v[0];
+}
+
+__device__ __forceinline__ double inclusive(double v)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const double y = __shfl_up_sync(~0u, v, d);
+        if (lane >= d) v += y;
+    }
+    return v;
+}
+
+// First index in [v0, v1) whose cumulative weight, from `c` on, passes the
+// mark; where rounding leaves it a last bit short, the last with any weight.
+// 16 groups of 32 at a time: one round of loads, then sums of groups, then
+// the one group that holds the index.
+__device__ __forceinline__ int search(const Weights &w, int v0, int v1, double c, double mark)
+{
+    const int lane = threadIdx.x & 31;
+    int last = v0;
+    for (int v = v0; v < v1; v += 32 * BLOCK) {
+        double x[BLOCK];
+#pragma unroll
+        for (int i = 0; i < BLOCK; ++i) {
+            const int j = v + 32 * i + lane;
+            x[i] = j < v1 ? w(j) : 0.0;
+            if (x[i] > 0.0) last = j;
+        }
+        const double all = group_sums(x), sum = lane < BLOCK ? all : 0.0;      // of groups, one a lane
+        const double upto = inclusive(sum);
+        const unsigned over = __ballot_sync(~0u, c + upto > mark && sum > 0.0);
+        if (over) {
+            const int group = __ffs(over) - 1;
+            const double start = c + __shfl_sync(~0u, upto - sum, group);
+            const int j = v + 32 * group + lane;
+            const double y = j < v1 ? w(j) : 0.0, run = inclusive(y);
+            const unsigned hit = __ballot_sync(~0u, start + run > mark && y > 0.0), any = __ballot_sync(~0u, y > 0.0);
+            return v + 32 * group + (hit ? __ffs(hit) - 1 : 31 - __clz(any));
+        }
+        c += __shfl_sync(~0u, upto, 31);
+    }
+    return __reduce_max_sync(~0u, last);
+}
+
+__global__ void __launch_bounds__(THREADS, 2) verify_kernel(VerifyArgs a)
 {
     __shared__ double part[WARPS];
-    __shared__ double cta_sum;
+    __shared__ double cta_sum[2];
     __shared__ int accepted_s;
     cg::cluster_group cluster = cg::this_cluster();
     const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -60,25 +121,26 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(VerifyArgs a)
     allow_dependents();
 
     int nd = a.n_draft[b];
+    const float u_last = a.u[(size_t)b * (K + 1) + K];
+    if (warp == 0) {                                                   // one lane a draft: K <= 31
+        int x = -1;
+        float u = 0.0f, p = 0.0f, q = 1.0f;
+        if (lane < K) {
+            x = a.draft[(size_t)b * K + lane];
+            u = a.u[(size_t)b * (K + 1) + lane];
+            if (x >= 0 && x < V) {
+                p = a.target[((size_t)b * (K + 1) + lane) * V + x];
+                if (a.probs) q = a.probs[((size_t)b * K + lane) * V + x];
+            }
+        }
+        if (rank == 0 && lane < min(nd, K) && (x < 0 || x >= V)) set_error(a.error, CSA2_DEV_BAD_INDEX);
+        const bool kept = lane < min(nd, K) && x >= 0 && x < V && (double)u * (double)q < (double)p;
+        const int n = __ffs(__ballot_sync(~0u, !kept)) - 1;            // lane 31 keeps nothing
+        if (lane == 0) accepted_s = n;
+    }
     if (nd < 0 || nd > K) {
         if (rank == 0 && threadIdx.x == 0) set_error(a.error, CSA2_DEV_BAD_REQUEST);
         nd = max(0, min(nd, K));
-    }
-    if (warp == 0) {                                                   // one lane a draft: K <= 31
-        bool refused = lane >= nd;
-        if (lane < nd) {
-            const int x = a.draft[(size_t)b * K + lane];
-            if (x < 0 || x >= V) {
-                if (rank == 0) set_error(a.error, CSA2_DEV_BAD_INDEX);
-                refused = true;
-            } else {
-                const double p = a.target[((size_t)b * (K + 1) + lane) * V + x];
-                const double q = a.probs ? a.probs[((size_t)b * K + lane) * V + x] : 1.0f;
-                refused = !((double)a.u[(size_t)b * (K + 1) + lane] * q < p);
-            }
-        }
-        const int n = __ffs(__ballot_sync(~0u, refused)) - 1;          // lane 31 always refuses
-        if (lane == 0) accepted_s = n;
     }
     __syncthreads();
     const int n = accepted_s;
@@ -88,76 +150,73 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(VerifyArgs a)
     w.q = w.residual && a.probs ? a.probs + ((size_t)b * K + n) * V : nullptr;
     w.x = w.residual ? a.draft[(size_t)b * K + n] : -1;
 
-    // piece of this warp: contiguous, a multiple of 32 so that rows stay aligned with one another
-    const int per = ((V + nc * WARPS - 1) / (nc * WARPS) + 31) & ~31;
-    const int v0 = min(V, (rank * WARPS + warp) * per), v1 = min(V, v0 + per);
-    double before = 0.0, total = 0.0;
+    // piece of this warp: contiguous, whole blocks of 512; lane i keeps the sum of its i-th run of blocks
+    const int blocks = (V + nc * WARPS * BLOCK * 32 - 1) / (nc * WARPS * BLOCK * 32), run = (blocks + 31) / 32 * BLOCK * 32;
+    const int per = blocks * BLOCK * 32;
+    const int64_t begin = (int64_t)(rank * WARPS + warp) * per;
+    const int v0 = (int)min((int64_t)V, begin), v1 = (int)min((int64_t)V, begin + per);
+    double before = 0.0, after = 0.0, total = 0.0, upto = 0.0, sums = 0.0;
     for (int pass = 0; pass < 2; ++pass) {
-        double s = 0.0;
-        for (int v = v0 + lane; v < v1; v += 32 * UNROLL) {
-            float pv[UNROLL], qv[UNROLL];
+        sums = 0.0;
+        for (int r = 0; v0 + (int64_t)r * run < v1; ++r) {
+            double s = 0.0;
+            const int e = min(v1, v0 + (r + 1) * run);
+            for (int v = v0 + r * run + lane; v < e; v += 32 * BLOCK) {
+                float pv[BLOCK], qv[BLOCK];
 #pragma unroll
-            for (int i = 0; i < UNROLL; ++i) {
-                const int j = v + 32 * i;
-                pv[i] = j < v1 ? w.p[j] : 0.0f;
-                qv[i] = w.residual && j < v1 ? w.draft(j) : 0.0f;
+                for (int i = 0; i < BLOCK; ++i) {
+                    const int j = v + 32 * i;
+                    pv[i] = j < e ? w.p[j] : 0.0f;
+                    qv[i] = w.residual && j < e ? w.draft(j) : 0.0f;
+                }
+#pragma unroll
+                for (int i = 0; i < BLOCK; ++i) s += w.of(pv[i], qv[i]);
             }
-#pragma unroll
-            for (int i = 0; i < UNROLL; ++i) s += w.of(pv[i], qv[i]);
+            s = warp_sum(s);
+            if (lane == r) sums = s;
         }
-        s = warp_sum(s);
-        if (lane == 0) part[warp] = s;
+        upto = inclusive(sums);
+        if (lane == 31) part[warp] = upto;
         __syncthreads();
-        if (threadIdx.x == 0) {
-            double t = 0.0;
-            for (int i = 0; i < WARPS; ++i) t += part[i];
-            cta_sum = t;
+        if (warp == 0) {
+            const double t = inclusive(lane < WARPS ? part[lane] : 0.0);
+            if (lane == 31) cta_sum[pass] = t;
         }
         cluster.sync();
-        before = total = 0.0;
-        for (int r = 0; r < nc; ++r) {
-            const double t = *cluster.map_shared_rank(&cta_sum, r);
-            if (r < rank) before += t;
-            total += t;
+        const double theirs = lane < nc ? *cluster.map_shared_rank(&cta_sum[pass], lane) : 0.0;
+        total = 0.0;
+        for (int r = 0; r < nc; ++r) {                                 // one after another: CTAs meet without a gap
+            if (r == rank) before = total;
+            total += __shfl_sync(~0u, theirs, r);
+            if (r == rank) after = total;
         }
-        cluster.sync();                                                // the sums are read: they may change, or the CTA end
         if (total > 0.0 || !w.residual) break;
         w.residual = false;                                            // p <= q everywhere: what is left is p itself
+        __syncthreads();                                               // part is read
     }
+    // The others may still be reading this CTA's sum: it stays until all have arrived here.
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+
     // The CTA whose sums straddle the mark holds the drawn index; in it, the
     // first warp whose running end passes the mark, or, where the warps' sums
-    // round a last bit below the CTA's, the last warp with any weight.
-    // Without a finite positive total (rows of zeros, NaN) it is the last token.
-    const double mark = fmin(fmax((double)a.u[(size_t)b * (K + 1) + K], 0.0), 1.0 - 0x1p-24) * total;
+    // round a last bit below the CTA's, the last warp with any weight; in that
+    // the run of blocks, likewise.  Without a finite positive total (rows of
+    // zeros, NaN) it is the last token.
+    const double mark = fmin(fmax((double)u_last, 0.0), 1.0 - 0x1p-24) * total;
     int *tokens = a.tokens + (size_t)b * (K + 1);
     if (total > 0.0 && total < INFINITY) {
-        int chosen = -1, any = -1;
-        double at = before, c = before;
-        for (int i = 0; i < WARPS; ++i) {
-            if (chosen < 0 && part[i] > 0.0) {
-                any = i;
-                c = at;
-                if (at + part[i] > mark) chosen = i;
+        if (before <= mark && mark < after) {
+            const double here = lane < WARPS ? part[lane] : 0.0, end = before + inclusive(here);
+            const unsigned over = __ballot_sync(~0u, end > mark && here > 0.0), any = __ballot_sync(~0u, here > 0.0);
+            const int chosen = over ? __ffs(over) - 1 : 31 - __clz(any);
+            if (warp == chosen) {
+                const double start = __shfl_sync(~0u, end - here, chosen);
+                const unsigned o = __ballot_sync(~0u, start + upto > mark && sums > 0.0), s = __ballot_sync(~0u, sums > 0.0);
+                const int r = o ? __ffs(o) - 1 : 31 - __clz(s);
+                const double c = start + __shfl_sync(~0u, upto - sums, r);
+                const int x = search(w, v0 + r * run, min(v1, v0 + (r + 1) * run), c, mark);
+                if (lane == 0) tokens[n] = x;
             }
-            at += part[i];
-        }
-        if (chosen < 0) chosen = any;
-        if (before <= mark && mark < before + cta_sum && warp == chosen) {
-            int hit = -1, last = v0;
-            for (int v = v0; v < v1 && hit < 0; v += 32) {
-                const double x = v + lane < v1 ? w(v + lane) : 0.0;
-                double s = x;
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const double y = __shfl_up_sync(~0u, s, d);
-                    if (lane >= d) s += y;
-                }
-                const unsigned over = __ballot_sync(~0u, c + s > mark && x > 0.0), some = __ballot_sync(~0u, x > 0.0);
-                if (over) hit = v + __ffs(over) - 1;
-                if (some) last = v + 31 - __clz(some);
-                c += __shfl_sync(~0u, s, 31);
-            }
-            if (lane == 0) tokens[n] = hit >= 0 ? hit : last;          // likewise a last bit short
         }
     } else if (rank == 0 && threadIdx.x == 0) {
         set_error(a.error, CSA2_DEV_BAD_REQUEST);
@@ -166,14 +225,19 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(VerifyArgs a)
     if (rank == 0 && threadIdx.x <= K && (int)threadIdx.x != n)
         tokens[threadIdx.x] = (int)threadIdx.x < n ? a.draft[(size_t)b * K + threadIdx.x] : -1;
     if (rank == 0 && threadIdx.x == 0) a.n_accepted[b] = n;
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 }  // namespace
 
 cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t st)
 {
+    // As many CTAs to a request as can all be at work (two on each of 148
+    // SMs), and no more than its row has blocks for.
+    int nc = MAX_CLUSTER;
+    while (nc > 1 && ((int64_t)a.batch * nc > 2 * 148 || a.vocab < nc * WARPS * 32 * BLOCK / 2)) nc /= 2;
     LaunchScope scope(-1, st);
-    const int nc = a.vocab >= 16384 ? MAX_CLUSTER : 1;
     return launch_pdl_cluster(verify_kernel, dim3((unsigned)a.batch * nc), dim3(THREADS), 0, st, nc, a);
 }
 
