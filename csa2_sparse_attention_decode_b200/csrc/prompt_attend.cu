@@ -108,6 +108,7 @@ struct Args {
     float *part_o;                             // [slots][RT][D]
     float2 *part_ml;                           // [slots][RT]
     int32_t *prefix;                           // [tiles + 1] units before a row tile
+    int32_t *starts;                           // [CTAS] first unit of each CTA; one without any: the units' number
 };
 
 // Tokens of the packed batch that belong to a request; the rows behind them are left alone.
@@ -815,6 +816,7 @@ __device__ void deal_units(const Args &a, Misc *m, int *before)
             const int mid = (b + e) >> 1;
             if (before[mid] <= u0) b = mid; else e = mid;
         }
+        a.starts[blockIdx.x] = u1 > u0 ? (int)u0 : total;
         *reinterpret_cast<Share *>(m->red) = {u1 - u0, b, (int)(u0 - before[b])};
     }
 }
@@ -891,40 +893,52 @@ prompt_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     }
 }
 
-// Joins the parts of the row tiles that several CTAs of `grid` shared.  A CTA
+// Joins the parts of the row tiles that several CTAs shared.  A CTA
 // takes four rows x 128 channels; blockDim.y groups of threads share the parts.
 constexpr int JOIN_GROUPS = 8;
 template <bool F32>
-__global__ void __launch_bounds__(128 * JOIN_GROUPS) prompt_join_kernel(const Args a, int grid)
+__global__ void __launch_bounds__(128 * JOIN_GROUPS) prompt_join_kernel(const Args a)
 {
     grid_dependency_wait();
     allow_dependents();
     const int tile = blockIdx.x / (RT / 4), i = 4 * (blockIdx.x % (RT / 4));
     const int c = blockIdx.y, d = 128 * c + threadIdx.x, group = threadIdx.y, groups = blockDim.y;
-    const int64_t total = a.prefix[a.tiles], u0 = a.prefix[tile], u1 = a.prefix[tile + 1];
+    const int u0 = a.prefix[tile], u1 = a.prefix[tile + 1];
     const int64_t row = (int64_t)tile * RT + i, live = (int64_t)live_tokens(a) * a.heads;
-    if (u1 == u0 || row >= live) return;
-    const int64_t ctas = min((int64_t)grid, total);
-    const int c0 = (int)(((u0 + 1) * ctas - 1) / total), c1 = (int)((u1 * ctas - 1) / total);
-    if (c0 == c1) return;                                              // one CTA had all of it
+    // CTAs c0 .. c1 began at or before the row tile's first unit, and before its end
+    const int tid = group * 128 + threadIdx.x, threads = groups * 128;
+    int c0 = -1, c1 = -1, start0 = 0;
+    for (int k = 0; k < CTAS; k += threads) {
+        const int start = k + tid < CTAS ? a.starts[k + tid] : INT32_MAX;
+        c0 += __syncthreads_count(start <= u0);
+        c1 += __syncthreads_count(start < u1);
+    }
+    if (u1 == u0 || row >= live || c0 == c1) return;                   // one CTA had all of it
+    start0 = a.starts[c0];
     // A CTA keeps the part of the row tile that it began with in its first
     // slot, a later one in its second; only the first of these CTAs began before.
-    const size_t first = 2 * (size_t)c0 + (total * c0 / ctas >= u0 ? 0 : 1);
+    const size_t first = 2 * (size_t)c0 + (start0 == u0 ? 0 : 1);
     const int n = c1 - c0 + 1;
     __shared__ float weight[4][CTAS], inv[4];
     __shared__ float4 sums[JOIN_GROUPS][128];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (group == 0) {                                                  // warp w: weights of row i + w
+        constexpr int N = (CTAS + 31) / 32;
+        float2 ml[N];
         float top = -INFINITY, sum = 0.0f;
-        for (int k = lane; k < n; k += 32)
-            top = fmaxf(top, a.part_ml[(k ? 2 * (size_t)(c0 + k) : first) * RT + i + warp].x);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int k = lane + 32 * j;
+            ml[j] = k < n ? a.part_ml[(k ? 2 * (size_t)(c0 + k) : first) * RT + i + warp] : make_float2(-INFINITY, 0.0f);
+            top = fmaxf(top, ml[j].x);
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-        for (int k = lane; k < n; k += 32) {
-            const float2 ml = a.part_ml[(k ? 2 * (size_t)(c0 + k) : first) * RT + i + warp];
-            const float w = ml.x == -INFINITY ? 0.0f : ex2(ml.x - top);
-            weight[warp][k] = w;
-            if (ml.x != -INFINITY) sum += w * ml.y;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float w = ml[j].x == -INFINITY ? 0.0f : ex2(ml[j].x - top);
+            if (lane + 32 * j < n) weight[warp][lane + 32 * j] = w;
+            if (ml[j].x != -INFINITY) sum += w * ml[j].y;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
@@ -936,7 +950,7 @@ __global__ void __launch_bounds__(128 * JOIN_GROUPS) prompt_join_kernel(const Ar
     }
     __syncthreads();
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
+#pragma unroll 10
     for (int k = group; k < n; k += groups) {
         const float4 v = *reinterpret_cast<const float4 *>(a.part_o + (k ? 2 * (size_t)(c0 + k) : first) * RT * D + part_at(i, d));
         o.x += weight[0][k] * v.x;
@@ -969,14 +983,15 @@ __global__ void __launch_bounds__(128 * JOIN_GROUPS) prompt_join_kernel(const Ar
 constexpr int SLOTS = 2 * CTAS;
 
 struct Layout {
-    size_t o, ml, prefix, bytes;
+    size_t o, ml, prefix, starts, bytes;
 };
 constexpr Layout layout()
 {
     Layout l = {};
     l.ml = sizeof(float) * (size_t)SLOTS * RT * D;
     l.prefix = l.ml + sizeof(float2) * (size_t)SLOTS * RT;
-    l.bytes = (l.prefix + sizeof(int32_t) * (MAX_SPLIT_TILES + 1) + 255) & ~(size_t)255;
+    l.starts = l.prefix + sizeof(int32_t) * (MAX_SPLIT_TILES + 1);
+    l.bytes = (l.starts + sizeof(int32_t) * CTAS + 255) & ~(size_t)255;
     return l;
 }
 
@@ -1020,7 +1035,7 @@ cudaError_t launch_variant(const CUtensorMap &map_q, const CUtensorMap &map_k, c
     LaunchScope scope(-1, st);
     // about 8 parts to a group of threads, if every SM works on the same few row tiles
     const int groups = std::max(1, std::min(JOIN_GROUPS, grid / (8 * a.tiles)));
-    return launch_pdl(prompt_join_kernel<SPLIT_P>, dim3(a.tiles * (RT / 4), CHUNKS), dim3(128, groups), 0, st, a, grid);
+    return launch_pdl(prompt_join_kernel<SPLIT_P>, dim3(a.tiles * (RT / 4), CHUNKS), dim3(128, groups), 0, st, a);
 }
 
 }  // namespace
@@ -1052,6 +1067,7 @@ cudaError_t launch_prompt_attend(const PromptArgs &p, cudaStream_t st)
     a.part_o = (float *)((char *)p.ws + l.o);
     a.part_ml = (float2 *)((char *)p.ws + l.ml);
     a.prefix = (int32_t *)((char *)p.ws + l.prefix);
+    a.starts = (int32_t *)((char *)p.ws + l.starts);
     CUtensorMap map_q, map_k, map_out;
     // Without keys the latents' map covers a row of q that every mask leaves out.
     if (!make_map(&map_q, p.q, (int64_t)p.n_q * p.heads, D, RT, 8) ||
