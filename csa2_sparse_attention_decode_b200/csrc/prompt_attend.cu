@@ -635,119 +635,120 @@ __device__ void softmax(const Args &a, Misc *m, uint8_t *sm)
             wait(m, &m->s_full, unit & 1);                             // given up: finish the segment, then leave
             fence_after_sync();
             float x[32];
-            {
-                uint32_t raw[32];
-                tmem_ld32(tb + S_COL + 32 * half, raw);
-                tmem_ld_wait();
+            bool exact = k == 0 && !g.uniform;                         // find the rows' maxima first
+            for (;;) {
+                {
+                    uint32_t raw[32];
+                    tmem_ld32(tb + S_COL + 32 * half, raw);
+                    tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(raw[j]);
-            }
-            const bool cleared = DEAL == SLIDING && (m->cleared[0] | m->cleared[1] | m->cleared[2] | m->cleared[3]);
-            if (key0 < g.max_lo || key0 + KT > g.min_hi || cleared) {
-                // A latent that is not finite gives no finite score at all.
-                // A masked weight of zero would not keep it out of O, so it
-                // is cleared, and the rows that do see it become NaN.
-                const int key = key0 + ((row - g.turn) & (KT - 1));
-                float least = INFINITY;
-#pragma unroll
-                for (int j = 0; j < 32; ++j) least = fminf(least, fabsf(x[j]));
-                const bool all = !(least < INFINITY);
-                bool poison = cleared && (m->cleared[row >> 5] >> (row & 31) & 1);     // this key's latent is not finite
-                if (soft_any(all)) {
-                    bad_key[half * KT + row] = all;
-                    soft_sync();
-                    const bool found = bad_key[row] && bad_key[KT + row];
-                    soft_sync();
-                    if (DEAL == SLIDING && found && half == 0) atomicOr(&m->cleared[row >> 5], 1u << (row & 31));
-                    poison |= found;
-                    if (found)
-#pragma unroll 1
-                        for (int i = 0; i < 4; ++i)
-#pragma unroll 1
-                            for (int c = 0; c < 8; ++c)
-                                *reinterpret_cast<uint4 *>(sm + K_OFF + (4 * half + i) * K_SLAB + row * 128 + 16 * c) =
-                                    make_uint4(0, 0, 0, 0);
+                    for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(raw[j]);
                 }
-                if (g.uniform) {                                       // one token's rows: the key is seen by all or none
-                    if (poison || key < g.max_lo || key >= g.min_hi) {
-                        const float v = key < g.max_lo || key >= g.min_hi ? masked : NAN;
+                const bool cleared = DEAL == SLIDING && (m->cleared[0] | m->cleared[1] | m->cleared[2] | m->cleared[3]);
+                if (key0 < g.max_lo || key0 + KT > g.min_hi || cleared) {
+                    // A latent that is not finite gives no finite score at
+                    // all.  A masked weight of zero would not keep it out of
+                    // O, so it is cleared, and the rows that do see it become
+                    // NaN.
+                    const int key = key0 + ((row - g.turn) & (KT - 1));
+                    float least = INFINITY;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) x[j] = v;
+                    for (int j = 0; j < 32; ++j) least = fminf(least, fabsf(x[j]));
+                    const bool all = !(least < INFINITY);
+                    bool poison = cleared && (m->cleared[row >> 5] >> (row & 31) & 1);     // this key's latent is not finite
+                    if (soft_any(all)) {
+                        bad_key[half * KT + row] = all;
+                        soft_sync();
+                        const bool found = bad_key[row] && bad_key[KT + row];
+                        soft_sync();
+                        if (DEAL == SLIDING && found && half == 0) atomicOr(&m->cleared[row >> 5], 1u << (row & 31));
+                        poison |= found;
+                        if (found)
+#pragma unroll 1
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll 1
+                                for (int c = 0; c < 8; ++c)
+                                    *reinterpret_cast<uint4 *>(sm + K_OFF + (4 * half + i) * K_SLAB + row * 128 + 16 * c) =
+                                        make_uint4(0, 0, 0, 0);
                     }
-                } else {
+                    if (g.uniform) {                                   // one token's rows: the key is seen by all or none
+                        if (poison || key < g.max_lo || key >= g.min_hi) {
+                            const float v = key < g.max_lo || key >= g.min_hi ? masked : NAN;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        if (poison) x[j] = NAN;
-                        if (key < lo[j] || key >= hi[j]) x[j] = masked;
+                            for (int j = 0; j < 32; ++j) x[j] = v;
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            if (poison) x[j] = NAN;
+                            if (key < lo[j] || key >= hi[j]) x[j] = masked;
+                        }
                     }
                 }
-            }
-            // A row's first reference: any score near the maximum will do, so
-            // where all rows see the same keys the first of them gives it.
-            if (k == 0 && g.uniform) {
-                if (((row - g.turn) & (KT - 1)) == max(key0, g.max_lo) - key0)
+                if (exact) {
+                    float v[32];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) m->muse[32 * half + j] = x[j] * sl;
-                soft_sync();
-            }
-            bool rise = k == 0 && !g.uniform;
-            if (!rise) {
+                    for (int j = 0; j < 32; ++j) v[j] = x[j] * sl;
+                    m->red[warp & 3][32 * half + lane] = columns<true>(v);
+                    soft_sync();
+                    if (tid < RT) {
+                        const float top = fmaxf(fmaxf(m->red[0][tid], m->red[1][tid]), fmaxf(m->red[2][tid], m->red[3][tid]));
+                        const float old = m->muse[tid], now = fmaxf(old, top);
+                        m->fac[r][tid] = ex2(old - now);               // fresh and still fresh: 1; now seen: 0
+                        m->muse[tid] = now;
+                    }
+                    soft_sync();
+                    if (k > 0) {                                       // S follows the last O product: O is at rest
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) l[j] *= m->fac[r][32 * half + j];
+#pragma unroll 1
+                        for (int c = 0; c < CHUNKS; ++c) {
+                            uint32_t o[32];
+                            tmem_ld32(tb + O_COL + RT * c + 32 * half, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                o[j] = __float_as_uint(__uint_as_float(o[j]) * m->fac[r][32 * half + j]);
+                            tmem_st32(tb + O_COL + RT * c + 32 * half, o);
+                        }
+                        tmem_st_wait();
+                    }
+                } else if (k == 0) {
+                    // A row's first reference: any score near the maximum will
+                    // do, so where all rows see the same keys the first of
+                    // them gives it.
+                    if (((row - g.turn) & (KT - 1)) == max(key0, g.max_lo) - key0)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) m->muse[32 * half + j] = x[j] * sl;
+                    soft_sync();
+                }
                 float top = -INFINITY;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float4 mu = muse4[j];
-                    top = fmaxf(fmaxf(top, fmaf(x[4 * j], sl, -mu.x)), fmaf(x[4 * j + 1], sl, -mu.y));
-                    top = fmaxf(fmaxf(top, fmaf(x[4 * j + 2], sl, -mu.z)), fmaf(x[4 * j + 3], sl, -mu.w));
-                }
-                rise = soft_any(top > RISE);
-            }
-            if (rise) {
-                float v[32];
+                for (int c = 0; c < 4; ++c) {
+                    const float4 ma = muse4[2 * c], mb = muse4[2 * c + 1];
+                    const float mu[8] = {ma.x, ma.y, ma.z, ma.w, mb.x, mb.y, mb.z, mb.w};
+                    uint32_t h[4], e[4];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = x[j] * sl;
-                m->red[warp & 3][32 * half + lane] = columns<true>(v);
-                soft_sync();
-                if (tid < RT) {
-                    const float top = fmaxf(fmaxf(m->red[0][tid], m->red[1][tid]), fmaxf(m->red[2][tid], m->red[3][tid]));
-                    const float old = m->muse[tid], now = fmaxf(old, top);
-                    m->fac[r][tid] = ex2(old - now);                      // fresh and still fresh: 1; now seen: 0
-                    m->muse[tid] = now;
-                }
-                soft_sync();
-                if (k > 0) {                                           // S follows the last O product: O is at rest
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) l[j] *= m->fac[r][32 * half + j];
-#pragma unroll 1
-                    for (int c = 0; c < CHUNKS; ++c) {
-                        uint32_t o[32];
-                        tmem_ld32(tb + O_COL + RT * c + 32 * half, o);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            o[j] = __float_as_uint(__uint_as_float(o[j]) * m->fac[r][32 * half + j]);
-                        tmem_st32(tb + O_COL + RT * c + 32 * half, o);
+                    for (int i = 0; i < 4; ++i) {
+                        float &p0 = x[8 * c + 2 * i], &p1 = x[8 * c + 2 * i + 1];
+                        p0 = fmaf(p0, sl, -mu[2 * i]);
+                        p1 = fmaf(p1, sl, -mu[2 * i + 1]);
+                        top = fmaxf(fmaxf(top, p0), p1);
+                        p0 = ex2(p0);
+                        p1 = ex2(p1);
+                        h[i] = pack2(p0, p1);
+                        if (SPLIT_P) e[i] = pack2(p0 - __uint_as_float(h[i] << 16), p1 - __uint_as_float(h[i] & 0xffff0000u));
                     }
-                    tmem_st_wait();
+                    const uint32_t off = row * 128 + (((4 * half + c) ^ (row & 7)) << 4);
+                    *reinterpret_cast<uint4 *>(P + off) = make_uint4(h[0], h[1], h[2], h[3]);
+                    if (SPLIT_P) *reinterpret_cast<uint4 *>(P + P_BYTES + off) = make_uint4(e[0], e[1], e[2], e[3]);
                 }
+                // A score far above its reference, in any warp: once more, from the maxima.
+                if (exact || !soft_any(top > RISE)) break;
+                exact = true;
             }
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float4 ma = muse4[2 * c], mb = muse4[2 * c + 1];
-                const float mu[8] = {ma.x, ma.y, ma.z, ma.w, mb.x, mb.y, mb.z, mb.w};
-                uint32_t h[4], e[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float p0 = ex2(fmaf(x[8 * c + 2 * i], sl, -mu[2 * i]));
-                    const float p1 = ex2(fmaf(x[8 * c + 2 * i + 1], sl, -mu[2 * i + 1]));
-                    l[8 * c + 2 * i] += p0;
-                    l[8 * c + 2 * i + 1] += p1;
-                    h[i] = pack2(p0, p1);
-                    if (SPLIT_P) e[i] = pack2(p0 - __uint_as_float(h[i] << 16), p1 - __uint_as_float(h[i] & 0xffff0000u));
-                }
-                const uint32_t off = row * 128 + (((4 * half + c) ^ (row & 7)) << 4);
-                *reinterpret_cast<uint4 *>(P + off) = make_uint4(h[0], h[1], h[2], h[3]);
-                if (SPLIT_P) *reinterpret_cast<uint4 *>(P + P_BYTES + off) = make_uint4(e[0], e[1], e[2], e[3]);
-            }
+            for (int j = 0; j < 32; ++j) l[j] += x[j];
             fence_proxy_async_smem();
             fence_before_sync();
             __syncwarp();
