@@ -346,6 +346,10 @@ csa2_status csa2_norm_rope(int32_t n, int32_t dim, int32_t heads, const uint16_t
     const bool norm = !(flags & CSA2_ROPE_NO_NORM);
     if (norm && !(eps >= 0.0f)) return CSA2_ERR_INVALID_ARG;
     if (n == 0) return CSA2_OK;
+    // in place only where input and output rows are the same
+    if ((heads > 0 && q == q_out && n > 1 && q_stride != (int64_t)heads * dim) ||
+        (kv_heads > 0 && k && k == k_out && n > 1 && k_stride != (int64_t)kv_heads * dim))
+        return CSA2_ERR_INVALID_ARG;
     if (rot_dim > 0 && (!pos || !inv_freq)) return CSA2_ERR_INVALID_ARG;
     if (heads > 0 && (!q || !q_out || (norm && !q_weight) || q_stride < (int64_t)heads * dim || q_stride % 8 ||
                       !aligned(q, 16) || !aligned(q_out, 16) || !aligned(q_weight, 16)))

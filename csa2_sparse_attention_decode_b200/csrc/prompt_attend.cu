@@ -192,17 +192,29 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-// A wait that gives up after a limit, or as soon as another role has.
+// A wait that gives up after 2^28 polls or four seconds (a row tile over a
+// million keys takes 20 ms), or as soon as another role has.
+__device__ __forceinline__ uint64_t nanoseconds()
+{
+    uint64_t t;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    return t;
+}
 __device__ __forceinline__ bool wait(Misc *m, uint64_t *bar, uint32_t parity)
 {
-    for (uint32_t i = 0; i < (1u << 22); ++i) {
+    uint64_t start = 0;
+    for (uint32_t i = 0; i < (1u << 28); ++i) {
         if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 255) == 255 && *reinterpret_cast<volatile int *>(&m->abort)) return false;
+        if ((i & 1023) == 1023) {
+            if (*reinterpret_cast<volatile int *>(&m->abort)) return false;
+            const uint64_t now = nanoseconds();
+            if (start == 0) start = now;
+            if (now - start > 4000000000ull) break;
+        }
     }
     *reinterpret_cast<volatile int *>(&m->abort) = 1;
     return false;
 }
-
 __device__ __forceinline__ bool warp_wait(Misc *m, uint64_t *bar, uint32_t parity)
 {
     return __all_sync(~0u, wait(m, bar, parity));
@@ -293,8 +305,9 @@ __device__ void producer(const Args &a, Misc *m, uint8_t *sm, const CUtensorMap 
     if (DEAL == WHOLE) tile = a.tiles - 1 - tile;                      // later tokens see more: heavy row tiles first
     if (DEAL == SHARED) tile = share.tile, at = share.at;
     if (DEAL == SLIDING) {
-        tile = (int)((int64_t)a.tiles * blockIdx.x / gridDim.x);
-        last = (int)((int64_t)a.tiles * (blockIdx.x + 1) / gridDim.x);
+        const int64_t tiles = ((int64_t)live * a.heads + RT - 1) / RT;  // not a padded batch's empty end
+        tile = (int)(tiles * blockIdx.x / gridDim.x);
+        last = (int)(tiles * (blockIdx.x + 1) / gridDim.x);
     }
     int64_t left = DEAL == SHARED ? share.units : 0;
     Request req = {-1, 0, 0};
@@ -323,7 +336,7 @@ __device__ void producer(const Args &a, Misc *m, uint8_t *sm, const CUtensorMap 
                 tile -= gridDim.x;
                 break;
             }
-        } else if (tile < last && tile * RT / a.heads < live) {
+        } else if (tile < last) {
             g.tile = tile++;
             g.n = 1;
         }

@@ -259,6 +259,12 @@ def test_parts_join_through_the_log_sum_exp():
         assert ((out[t:t + 1].double() - o).abs() <= (2.0 ** -16 + 2 * err + 2.0 ** -18) * mag).all()
 
 
+def test_padded_batch_leaves_the_rest_alone():
+    # a captured batch's room with few live tokens, in every way of dealing the row tiles out
+    for heads, window, live in ((64, 128, 37), (64, 0, 37), (20, 0, 900), (20, 100, 5), (64, 128, 0)):
+        _check_all([live // 2, live - live // 2], [3, 0], heads, window, False, seed=live, extra_q=3000)
+
+
 @pytest.mark.slow
 def test_sizes_past_32_bits():
     # 66,001 tokens x 64 heads: more than 2^31 elements of q and of out

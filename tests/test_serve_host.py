@@ -1,5 +1,5 @@
 """Refusals of the calls around the layers (verification, token plan, head
-norm with rotation), made on the host before anything is enqueued."""
+norm with rotation, prompt attention), made on the host before anything is enqueued."""
 import ctypes as C
 
 import pytest
@@ -52,7 +52,30 @@ def test_norm_rope_refusals():
                 {"k": None}, {"kw": None}, {"ko": None, "kf": None}, {"ks": 504}, {"ks": 516}, {"pos": None},
                 {"freq": None}, {"q": odd}, {"qo": odd}, {"k": odd}, {"ko": odd}, {"kf": odd}, {"qw": odd}):
         assert call(**bad) == 1, bad
+    # in place over rows that lie apart
+    assert call(q=G, qo=G, qs=65 * 512) == 1
+    assert call(qo=C.c_void_p(256 * 300), k=G, ko=G, ks=1024) == 1
     assert call(n=0) == 0                      # nothing to do, nothing enqueued
+
+
+def test_prompt_attend_refusals():
+    f = csa2.lib.csa2_prompt_attend
+    odd = C.c_void_p(256 * 100 + 8)
+
+    def call(batch=2, cu_q=G, cu_k=G, n_q=100, n_k=300, heads=64, q=G, lat=G, stride=512, window=0, scale=0.1, out=G,
+             f32=0, lse=None, err=G, ws=G, ws_bytes=1 << 30):
+        return f(batch, cu_q, cu_k, n_q, n_k, heads, q, lat, stride, window, scale, out, f32, lse, err, ws, ws_bytes,
+                 None)
+
+    need = csa2.csa2_prompt_workspace_bytes(100, 64, 300)
+    for bad in ({"batch": 0}, {"n_q": -1}, {"n_k": -1}, {"heads": 0}, {"heads": 129}, {"window": -1}, {"cu_q": None},
+                {"cu_k": None}, {"q": None}, {"lat": None}, {"out": None}, {"err": None}, {"ws": None}, {"q": odd},
+                {"lat": odd}, {"out": odd}, {"ws": odd}, {"stride": 511}, {"stride": 516}, {"stride": 504},
+                {"ws_bytes": need - 1}, {"n_q": 1 << 25}, {"n_k": (1 << 31) - 1}):
+        assert call(**bad) == 1, bad
+    assert call(n_q=0, q=None, out=None, ws=None) == 0
+    assert csa2.csa2_prompt_workspace_bytes(0, 64, 300) == 0 == csa2.csa2_prompt_workspace_bytes(10, 129, 300)
+    assert csa2.csa2_prompt_workspace_bytes(1, 64, 128) == 256 == csa2.csa2_prompt_workspace_bytes(100000, 64, 100000)
 
 
 def test_bindings_refuse_wrong_types_shapes_and_places():
