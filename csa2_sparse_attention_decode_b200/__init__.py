@@ -327,6 +327,11 @@ def csa2_selftest_wait_timeout(error_word, polls: int = 1024, stream=None):
 
 
 # ---------------------------------------------------------------- around the layers
+# A step of a serving program makes these calls eagerly with small tensors,
+# where the host's time is the call's: one pass of cheap checks per argument.
+_F32, _I32, _B16 = torch.float32, torch.int32, torch.bfloat16
+
+
 def _typed(name, t, dtype, shape, dev):
     """The device pointer of t after its type, shape and device are checked (None passes)."""
     if t is None:
@@ -341,9 +346,9 @@ def _typed(name, t, dtype, shape, dev):
 
 
 def _here(t, dev):
-    if not t.is_cuda:
-        raise ValueError("libcsa2 takes device tensors")
     if t.get_device() != dev:
+        if not t.is_cuda:
+            raise ValueError("libcsa2 takes device tensors")
         raise ValueError("libcsa2 takes tensors of the current device")
     return t.data_ptr()
 
@@ -352,19 +357,28 @@ def _device():
     return torch.cuda.current_device() if torch.cuda.is_initialized() else -2      # -1 is the host
 
 
+def _stream_on(stream, dev):
+    if stream is None and _raw_stream is not None and dev >= 0:
+        return _raw_stream(dev)
+    return _stream(stream)
+
+
 def csa2_verify(target, probs, draft, n_draft, u, n_accepted, tokens, error, stream=None):
     """Accept drafted tokens draft [batch, k] against target [batch, k+1,
     vocab] f32 and the drafter's probs [batch, k, vocab] f32 (None: it named
     its tokens for certain) with random numbers u [batch, k+1]; n_accepted
     [batch] and tokens [batch, k+1] (kept drafts, drawn token, -1) receive the
     outcome."""
-    B, k1, V = (int(x) for x in target.shape)
-    f32, i32, dev = torch.float32, torch.int32, _device()
-    _check("csa2_verify", lib.csa2_verify(
-        B, k1 - 1, V, _typed("target", target, f32, (B, k1, V), dev), _typed("probs", probs, f32, (B, k1 - 1, V), dev),
-        _typed("draft", draft, i32, (B, k1 - 1), dev), _typed("n_draft", n_draft, i32, (B,), dev),
-        _typed("u", u, f32, (B, k1), dev), _typed("n_accepted", n_accepted, i32, (B,), dev),
-        _typed("tokens", tokens, i32, (B, k1), dev), _typed("error", error, i32, (1,), dev), _stream(stream)))
+    B, k1, V = target.shape
+    dev = _device()
+    st = lib.csa2_verify(
+        B, k1 - 1, V, _typed("target", target, _F32, (B, k1, V), dev),
+        _typed("probs", probs, _F32, (B, k1 - 1, V), dev), _typed("draft", draft, _I32, (B, k1 - 1), dev),
+        _typed("n_draft", n_draft, _I32, (B,), dev), _typed("u", u, _F32, (B, k1), dev),
+        _typed("n_accepted", n_accepted, _I32, (B,), dev), _typed("tokens", tokens, _I32, (B, k1), dev),
+        _typed("error", error, _I32, (1,), dev), _stream_on(stream, dev))
+    if st:
+        raise CSA2Error("csa2_verify", st)
 
 
 def csa2_plan_tokens(n_tokens, n_new, m, page_table, free_pages, n_free, n_free_out, cu_new, token_req, token_pos,
@@ -373,28 +387,32 @@ def csa2_plan_tokens(n_tokens, n_new, m, page_table, free_pages, n_free, n_free_
     n_tokens, n_new, m [batch]; page_table [batch, max_pages] and free_pages
     [n_pages] are updated; n_free, n_free_out [1]; cu_new [batch+1];
     token_req, token_pos, token_slot [max_new]."""
-    B, width = (int(x) for x in page_table.shape)
-    n_pages, room, i32, dev = int(free_pages.shape[0]), int(token_req.shape[0]), torch.int32, _device()
-    _check("csa2_plan_tokens", lib.csa2_plan_tokens(
-        B, width, n_pages, room, _typed("n_tokens", n_tokens, i32, (B,), dev), _typed("n_new", n_new, i32, (B,), dev),
-        _typed("m", m, i32, (B,), dev), _typed("page_table", page_table, i32, (B, width), dev),
-        _typed("free_pages", free_pages, i32, (n_pages,), dev), _typed("n_free", n_free, i32, (1,), dev),
-        _typed("n_free_out", n_free_out, i32, (1,), dev), _typed("cu_new", cu_new, i32, (B + 1,), dev),
-        _typed("token_req", token_req, i32, (room,), dev), _typed("token_pos", token_pos, i32, (room,), dev),
-        _typed("token_slot", token_slot, i32, (room,), dev), _typed("error", error, i32, (1,), dev), _stream(stream)))
+    B, width = page_table.shape
+    one, per, rows, dev = (1,), (B,), token_req.shape, _device()
+    n_pages = free_pages.shape[0]
+    st = lib.csa2_plan_tokens(
+        B, width, n_pages, rows[0], _typed("n_tokens", n_tokens, _I32, per, dev), _typed("n_new", n_new, _I32, per, dev),
+        _typed("m", m, _I32, per, dev), _typed("page_table", page_table, _I32, (B, width), dev),
+        _typed("free_pages", free_pages, _I32, (n_pages,), dev), _typed("n_free", n_free, _I32, one, dev),
+        _typed("n_free_out", n_free_out, _I32, one, dev), _typed("cu_new", cu_new, _I32, (B + 1,), dev),
+        _typed("token_req", token_req, _I32, (rows[0],), dev), _typed("token_pos", token_pos, _I32, rows, dev),
+        _typed("token_slot", token_slot, _I32, rows, dev), _typed("error", error, _I32, one, dev),
+        _stream_on(stream, dev))
+    if st:
+        raise CSA2Error("csa2_plan_tokens", st)
 
 
 def _heads(name, t, dev):
     """(pointer, heads, dim, token stride) of a bf16 [n, heads, dim] tensor whose
-    tokens may lie apart (a slice of a wider projection); None has no heads."""
-    if t is None:
-        return None, 0, 0, 0
-    if t.dtype != torch.bfloat16 or t.dim() != 3:
+    tokens may lie apart (a slice of a wider projection)."""
+    if t.dtype is not _B16 or t.dim() != 3:
         raise ValueError(f"{name}: bfloat16 [n, heads, dim] expected, got {t.dtype} {tuple(t.shape)}")
-    n, h, d = (int(x) for x in t.shape)
-    if t.numel() and (t.stride(2) != 1 or (h > 1 and t.stride(1) != d)):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return _here(t, dev), h, d, t.stride(0) if n > 1 else h * d
+    n, h, d = t.shape
+    apart, head, chan = t.stride()
+    if chan != 1 or (h > 1 and head != d):
+        if t.numel():
+            raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return _here(t, dev), h, d, apart if n > 1 else h * d
 
 
 def csa2_norm_rope(q, k, pos, inv_freq, q_weight, k_weight, eps: float, q_out, k_out, k_out_f32=None, n_valid=None,
@@ -404,22 +422,23 @@ def csa2_norm_rope(q, k, pos, inv_freq, q_weight, k_weight, eps: float, q_out, k
     bf16, k_out_f32 f32 (one k output may be None).  pos [n] i32; inv_freq
     [rot_dim / 2] f32 or None; n_valid: device int32 [1] or None; flags:
     ROPE_HALVES | ROPE_INVERSE | ROPE_NO_NORM."""
+    dev = _device()
+    qp, h, dq, qs = (None, 0, 0, 0) if q is None else _heads("q", q, dev)
+    kp, g, dk, ks = (None, 0, 0, 0) if k is None else _heads("k", k, dev)
     if q is None and k is None:
         raise ValueError("csa2_norm_rope needs q or k")
-    dev = _device()
-    qp, h, dq, qs = _heads("q", q, dev)
-    kp, g, dk, ks = _heads("k", k, dev)
-    n, d = int((q if q is not None else k).shape[0]), dq or dk
-    if q is not None and k is not None and (dq != dk or int(k.shape[0]) != n):
+    n, d = (k if q is None else q).shape[0], dq or dk
+    if q is not None and k is not None and (dq != dk or k.shape[0] != n):
         raise ValueError("q and k differ in tokens or channels")
-    f32, i32, b16 = torch.float32, torch.int32, torch.bfloat16
-    rot = 0 if inv_freq is None else 2 * int(inv_freq.shape[0])
-    _check("csa2_norm_rope", lib.csa2_norm_rope(
-        n, d, h, qp, qs, _typed("q_weight", q_weight, f32, (d,), dev), _typed("q_out", q_out, b16, (n, h, d), dev), g, kp, ks,
-        _typed("k_weight", k_weight, f32, (d,), dev), _typed("k_out", k_out, b16, (n, g, d), dev),
-        _typed("k_out_f32", k_out_f32, f32, (n, g, d), dev), _typed("pos", pos, i32, (n,), dev),
-        _typed("inv_freq", inv_freq, f32, (rot // 2,), dev), rot, float(eps), int(flags),
-        _typed("n_valid", n_valid, i32, (1,), dev), _stream(stream)))
+    half = 0 if inv_freq is None else inv_freq.shape[0]
+    st = lib.csa2_norm_rope(
+        n, d, h, qp, qs, _typed("q_weight", q_weight, _F32, (d,), dev), _typed("q_out", q_out, _B16, (n, h, d), dev),
+        g, kp, ks, _typed("k_weight", k_weight, _F32, (d,), dev), _typed("k_out", k_out, _B16, (n, g, d), dev),
+        _typed("k_out_f32", k_out_f32, _F32, (n, g, d), dev), _typed("pos", pos, _I32, (n,), dev),
+        _typed("inv_freq", inv_freq, _F32, (half,), dev), 2 * half, eps, flags,
+        _typed("n_valid", n_valid, _I32, (1,), dev), _stream_on(stream, dev))
+    if st:
+        raise CSA2Error("csa2_norm_rope", st)
 
 
 def csa2_prompt_workspace_bytes(n_q: int, heads: int, n_k: int) -> int:
@@ -432,15 +451,18 @@ def csa2_prompt_attend(q, lat, cu_q, cu_k, window: int, scale: float, out, lse, 
     cu_q[b]..cu_q[b+1] and latents cu_k[b]..cu_k[b+1]; window 0 sees
     everything.  out like q, bf16 or f32; lse [n_q, heads] f32 or None; ws:
     uint8, csa2_prompt_workspace_bytes(n_q, heads, n_k)."""
-    n_q, heads = int(q.shape[0]), int(q.shape[1])
-    i32, b16, dev = torch.int32, torch.bfloat16, _device()
-    if lat.dtype != b16 or lat.dim() != 2 or lat.shape[1] != LATENT or (lat.numel() and lat.stride(1) != 1):
+    n_q, heads = q.shape[:2]
+    dev = _device()
+    if lat.dtype is not _B16 or lat.dim() != 2 or lat.shape[1] != LATENT or (lat.stride(1) != 1 and lat.numel()):
         raise ValueError(f"lat: rows of {LATENT} bfloat16 expected, got {lat.dtype} {tuple(lat.shape)}")
-    n_k, batch = int(lat.shape[0]), int(cu_q.shape[0]) - 1
-    fp32 = out.dtype == torch.float32
-    _check("csa2_prompt_attend", lib.csa2_prompt_attend(
-        batch, _typed("cu_q", cu_q, i32, (batch + 1,), dev), _typed("cu_k", cu_k, i32, (batch + 1,), dev), n_q, n_k, heads,
-        _typed("q", q, b16, (n_q, heads, LATENT), dev), _here(lat, dev), lat.stride(0) if n_k > 1 else LATENT, int(window),
-        float(scale), _typed("out", out, torch.float32 if fp32 else b16, (n_q, heads, LATENT), dev), int(fp32),
-        _typed("lse", lse, torch.float32, (n_q, heads), dev), _typed("error", error, i32, (1,), dev),
-        _typed("ws", ws, torch.uint8, (ws.numel(),), dev), ws.numel(), _stream(stream)))
+    n_k, cu, rows = lat.shape[0], cu_q.shape, (n_q, heads, LATENT)
+    fp32 = out.dtype is _F32
+    n_ws = ws.numel()
+    st = lib.csa2_prompt_attend(
+        cu[0] - 1, _typed("cu_q", cu_q, _I32, (cu[0],), dev), _typed("cu_k", cu_k, _I32, cu, dev), n_q, n_k, heads,
+        _typed("q", q, _B16, rows, dev), _here(lat, dev), lat.stride(0) if n_k > 1 else LATENT, window, scale,
+        _typed("out", out, _F32 if fp32 else _B16, rows, dev), fp32, _typed("lse", lse, _F32, (n_q, heads), dev),
+        _typed("error", error, _I32, (1,), dev), _typed("ws", ws, torch.uint8, (n_ws,), dev), n_ws,
+        _stream_on(stream, dev))
+    if st:
+        raise CSA2Error("csa2_prompt_attend", st)
