@@ -921,18 +921,25 @@ __global__ void __launch_bounds__(128 * JOIN_GROUPS) prompt_join_kernel(const Ar
     const int64_t row = (int64_t)tile * RT + i, live = (int64_t)live_tokens(a) * a.heads;
     // CTAs c0 .. c1 began at or before the row tile's first unit, and before its end
     const int tid = group * 128 + threadIdx.x, threads = groups * 128;
-    int c0 = -1, c1 = -1, start0 = 0;
+    int c0 = -1, c1 = -1, begins = 0;
     for (int k = 0; k < CTAS; k += threads) {
         const int start = k + tid < CTAS ? a.starts[k + tid] : INT32_MAX;
         c0 += __syncthreads_count(start <= u0);
         c1 += __syncthreads_count(start < u1);
+        begins |= __syncthreads_or(start == u0);
     }
     if (u1 == u0 || row >= live || c0 == c1) return;                   // one CTA had all of it
-    start0 = a.starts[c0];
     // A CTA keeps the part of the row tile that it began with in its first
     // slot, a later one in its second; only the first of these CTAs began before.
-    const size_t first = 2 * (size_t)c0 + (start0 == u0 ? 0 : 1);
+    const size_t first = 2 * (size_t)c0 + (begins ? 0 : 1);
     const int n = c1 - c0 + 1;
+    auto part = [&](int k) {
+        return *reinterpret_cast<const float4 *>(a.part_o + (k ? 2 * (size_t)(c0 + k) : first) * RT * D + part_at(i, d));
+    };
+    constexpr int EARLY = 6;                                           // on their way while the weights are formed
+    float4 early[EARLY];
+#pragma unroll
+    for (int j = 0; j < EARLY; ++j) early[j] = group + j * groups < n ? part(group + j * groups) : make_float4(0.f, 0.f, 0.f, 0.f);
     __shared__ float weight[4][CTAS], inv[4];
     __shared__ float4 sums[JOIN_GROUPS][128];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -964,14 +971,17 @@ __global__ void __launch_bounds__(128 * JOIN_GROUPS) prompt_join_kernel(const Ar
     }
     __syncthreads();
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 10
-    for (int k = group; k < n; k += groups) {
-        const float4 v = *reinterpret_cast<const float4 *>(a.part_o + (k ? 2 * (size_t)(c0 + k) : first) * RT * D + part_at(i, d));
+    auto add = [&](const float4 &v, int k) {
         o.x += weight[0][k] * v.x;
         o.y += weight[1][k] * v.y;
         o.z += weight[2][k] * v.z;
         o.w += weight[3][k] * v.w;
-    }
+    };
+#pragma unroll
+    for (int j = 0; j < EARLY; ++j)
+        if (group + j * groups < n) add(early[j], group + j * groups);
+#pragma unroll 8
+    for (int k = group + EARLY * groups; k < n; k += groups) add(part(k), k);
     if (groups > 1) {
         sums[group][threadIdx.x] = o;
         __syncthreads();
