@@ -60,6 +60,10 @@ constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float RISE = 32.0f;                  // how far (in log2) a score may pass the reference
 constexpr float FRESH = -3.0e38f;              // reference of a row that has seen no key: every score passes it
 constexpr int CTAS = 148;                      // one per SM
+// A share of the units ends at a row tile's border if one is this near: a part
+// costs its way through memory and the join (8 ragged tokens 30 us with 2,
+// 24 with 0 or 1; 400 tokens after 1000 latents 98 with 1, 101 with 0 or 2).
+constexpr int SNAP = 1;
 constexpr int MAX_SPLIT_TILES = 2 * THREADS;   // row tiles that the split path plans in every CTA
 
 // How row tiles meet the CTAs.
@@ -92,8 +96,7 @@ constexpr size_t SMEM_BYTES = P_OFF + 2 * P_BYTES + sizeof(Misc);
 static_assert(SMEM_BYTES <= 232448, "shared memory of one CTA");
 
 struct Share {                                 // SHARED: what deal_units() leaves for the producer, in Misc::red
-    int64_t units;
-    int tile, at;
+    int units, tile, at;
 };
 
 struct Args {
@@ -107,8 +110,7 @@ struct Args {
     int32_t *error;
     float *part_o;                             // [slots][RT][D]
     float2 *part_ml;                           // [slots][RT]
-    int32_t *prefix;                           // [tiles + 1] units before a row tile
-    int32_t *starts;                           // [CTAS] first unit of each CTA; one without any: the units' number
+    int4 *shared;                              // [CTAS] row tiles that several CTAs share: tile, first CTA, CTAs (0: none), slot
 };
 
 // Tokens of the packed batch that belong to a request; the rows behind them are left alone.
@@ -309,7 +311,7 @@ __device__ void producer(const Args &a, Misc *m, uint8_t *sm, const CUtensorMap 
         tile = (int)(tiles * blockIdx.x / gridDim.x);
         last = (int)(tiles * (blockIdx.x + 1) / gridDim.x);
     }
-    int64_t left = DEAL == SHARED ? share.units : 0;
+    int left = DEAL == SHARED ? share.units : 0;
     Request req = {-1, 0, 0};
     int base = 0, top = -1;                                            // SLIDING: the ring holds keys [top - 128, top)
     uint32_t unit = 0;
@@ -320,7 +322,7 @@ __device__ void producer(const Args &a, Misc *m, uint8_t *sm, const CUtensorMap 
                 const int total = key_tiles(a, live, tile, at, g.key0);
                 if (total - at <= 0) continue;
                 g.tile = tile;
-                g.n = (int)min(left, (int64_t)(total - at));
+                g.n = min(left, total - at);
                 if (g.n < total) g.slot = 2 * blockIdx.x + (s == 0 ? 0 : 1);
                 left -= g.n;
                 ++tile;
@@ -803,7 +805,7 @@ __device__ void deal_units(const Args &a, Misc *m, int *before)
         const int y = __shfl_up_sync(~0u, x, d);
         if (lane >= d) x += y;
     }
-    int *sums = reinterpret_cast<int *>(m->red);
+    int *sums = reinterpret_cast<int *>(m->red) + sizeof(Share) / sizeof(int);
     if (lane == 31) sums[warp] = x;
     __syncthreads();
     int add = 0, total = 0;
@@ -816,22 +818,50 @@ __device__ void deal_units(const Args &a, Misc *m, int *before)
     if (2 * tid + 1 < a.tiles) before[2 * tid + 1] = mine + n[0];
     if (tid == 0) before[a.tiles] = total;
     __syncthreads();
-    if (blockIdx.x == 0)
-        for (int i = tid; i <= a.tiles; i += THREADS) a.prefix[i] = before[i];
-    if (tid == 0) {
-        const int64_t ctas = min((int64_t)gridDim.x, (int64_t)total);
-        int64_t u0 = 0, u1 = 0;
-        if (blockIdx.x < ctas) {
-            u0 = (int64_t)total * blockIdx.x / ctas;
-            u1 = (int64_t)total * (blockIdx.x + 1) / ctas;
-        }
+    // First unit of CTA c: its fair share's, or a near end of the row tile there.
+    const int ctas = min((int)gridDim.x, total);
+    auto start = [&](int c, int &tile) {
+        const int u = c < ctas ? (int)((int64_t)total * c / ctas) : total;
         int b = 0, e = a.tiles;
         while (e - b > 1) {
             const int mid = (b + e) >> 1;
-            if (before[mid] <= u0) b = mid; else e = mid;
+            if (before[mid] <= u) b = mid; else e = mid;
         }
-        a.starts[blockIdx.x] = u1 > u0 ? (int)u0 : total;
-        *reinterpret_cast<Share *>(m->red) = {u1 - u0, b, (int)(u0 - before[b])};
+        const int off = u - before[b], rest = before[b + 1] - u;
+        const int at = off <= SNAP && off <= rest ? before[b] : rest <= SNAP ? before[b + 1] : u;
+        while (b + 1 < a.tiles && before[b + 1] <= at) ++b;
+        tile = b;
+        return at;
+    };
+    if (tid == 0) {
+        int tile, next;
+        const int u0 = start(blockIdx.x, tile), u1 = start(blockIdx.x + 1, next);
+        *reinterpret_cast<Share *>(m->red) = {u1 - u0, tile, u0 - before[tile]};
+    }
+    // For the join, by the first CTA: row tile after row tile, the CTAs that
+    // begin inside it.  The one before them has its beginning, as a part in
+    // the second of its slots unless it began there.
+    int *tiles = before + a.tiles + 1, *starts = tiles + CTAS;
+    if (blockIdx.x == 0 && tid < CTAS) {
+        int tile;
+        starts[tid] = start(tid, tile);
+        tiles[tid] = starts[tid] > before[tile] && starts[tid] < total ? tile : -1;    // -1: at a border
+    }
+    __syncthreads();
+    if (blockIdx.x == 0) {
+        const int tile = tid < CTAS ? tiles[tid] : -1;
+        const bool opens = tile >= 0 && tiles[tid - 1] != tile;        // CTA 0 begins at a border
+        const uint32_t mask = __ballot_sync(~0u, opens);
+        if (lane == 0) sums[warp] = __popc(mask);
+        if (tid < CTAS) a.shared[tid] = make_int4(0, 0, 0, 0);
+        __syncthreads();
+        if (opens) {
+            int rank = __popc(mask & ((1u << lane) - 1)), n = 2;
+            for (int w = 0; w < warp; ++w) rank += sums[w];
+            while (tid + n - 1 < CTAS && tiles[tid + n - 1] == tile) ++n;
+            a.shared[rank] = make_int4(tile, tid - 1, n, 2 * (tid - 1) + (starts[tid - 1] == before[tile] ? 0 : 1));
+        }
+        __syncthreads();
     }
 }
 
@@ -907,39 +937,30 @@ prompt_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     }
 }
 
-// Joins the parts of the row tiles that several CTAs shared.  A CTA
-// takes four rows x 128 channels; blockDim.y groups of threads share the parts.
+// Joins the parts of the row tiles that several CTAs shared.  A CTA takes four
+// rows x `chunks` times 128 channels; blockDim.y groups of threads share the
+// parts.
 constexpr int JOIN_GROUPS = 8;
 template <bool F32>
-__global__ void __launch_bounds__(128 * JOIN_GROUPS) prompt_join_kernel(const Args a)
+__global__ void __launch_bounds__(128 * JOIN_GROUPS) prompt_join_kernel(const Args a, int chunks)
 {
     grid_dependency_wait();
     allow_dependents();
-    const int tile = blockIdx.x / (RT / 4), i = 4 * (blockIdx.x % (RT / 4));
-    const int c = blockIdx.y, d = 128 * c + threadIdx.x, group = threadIdx.y, groups = blockDim.y;
-    const int u0 = a.prefix[tile], u1 = a.prefix[tile + 1];
+    const int4 job = a.shared[blockIdx.x / (RT / 4)];
+    const int tile = job.x, c0 = job.y, n = job.z, first = job.w;
+    const int i = 4 * (blockIdx.x % (RT / 4)), group = threadIdx.y, groups = blockDim.y;
     const int64_t row = (int64_t)tile * RT + i, live = (int64_t)live_tokens(a) * a.heads;
-    // CTAs c0 .. c1 began at or before the row tile's first unit, and before its end
-    const int tid = group * 128 + threadIdx.x, threads = groups * 128;
-    int c0 = -1, c1 = -1, begins = 0;
-    for (int k = 0; k < CTAS; k += threads) {
-        const int start = k + tid < CTAS ? a.starts[k + tid] : INT32_MAX;
-        c0 += __syncthreads_count(start <= u0);
-        c1 += __syncthreads_count(start < u1);
-        begins |= __syncthreads_or(start == u0);
-    }
-    if (u1 == u0 || row >= live || c0 == c1) return;                   // one CTA had all of it
-    // A CTA keeps the part of the row tile that it began with in its first
-    // slot, a later one in its second; only the first of these CTAs began before.
-    const size_t first = 2 * (size_t)c0 + (begins ? 0 : 1);
-    const int n = c1 - c0 + 1;
-    auto part = [&](int k) {
-        return *reinterpret_cast<const float4 *>(a.part_o + (k ? 2 * (size_t)(c0 + k) : first) * RT * D + part_at(i, d));
+    if (n == 0 || row >= live) return;
+    // slot of part k; the CTAs behind the first began with theirs
+    auto slot = [&](int k) { return (size_t)(k ? 2 * (c0 + k) : first); };
+    auto part = [&](int k, int d) {
+        return *reinterpret_cast<const float4 *>(a.part_o + slot(k) * RT * D + part_at(i, d));
     };
+    int d = 128 * chunks * blockIdx.y + threadIdx.x;
     constexpr int EARLY = 6;                                           // on their way while the weights are formed
     float4 early[EARLY];
 #pragma unroll
-    for (int j = 0; j < EARLY; ++j) early[j] = group + j * groups < n ? part(group + j * groups) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 0; j < EARLY; ++j) early[j] = group + j * groups < n ? part(group + j * groups, d) : make_float4(0.f, 0.f, 0.f, 0.f);
     __shared__ float weight[4][CTAS], inv[4];
     __shared__ float4 sums[JOIN_GROUPS][128];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -950,7 +971,7 @@ __global__ void __launch_bounds__(128 * JOIN_GROUPS) prompt_join_kernel(const Ar
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const int k = lane + 32 * j;
-            ml[j] = k < n ? a.part_ml[(k ? 2 * (size_t)(c0 + k) : first) * RT + i + warp] : make_float2(-INFINITY, 0.0f);
+            ml[j] = k < n ? a.part_ml[slot(k) * RT + i + warp] : make_float2(-INFINITY, 0.0f);
             top = fmaxf(top, ml[j].x);
         }
 #pragma unroll
@@ -966,56 +987,64 @@ __global__ void __launch_bounds__(128 * JOIN_GROUPS) prompt_join_kernel(const Ar
         if (lane == 0) {
             const bool none = top == -INFINITY;
             inv[warp] = none ? 0.0f : 1.0f / sum;
-            if (c == 0 && a.lse && row + warp < live) a.lse[row + warp] = none ? -INFINITY : (top + log2f(sum)) * LN2;
+            if (blockIdx.y == 0 && a.lse && row + warp < live)
+                a.lse[row + warp] = none ? -INFINITY : (top + log2f(sum)) * LN2;
         }
     }
     __syncthreads();
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](const float4 &v, int k) {
-        o.x += weight[0][k] * v.x;
-        o.y += weight[1][k] * v.y;
-        o.z += weight[2][k] * v.z;
-        o.w += weight[3][k] * v.w;
-    };
+    for (int c = 0; c < chunks; ++c, d += 128) {
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](const float4 &v, int k) {
+            o.x += weight[0][k] * v.x;
+            o.y += weight[1][k] * v.y;
+            o.z += weight[2][k] * v.z;
+            o.w += weight[3][k] * v.w;
+        };
 #pragma unroll
-    for (int j = 0; j < EARLY; ++j)
-        if (group + j * groups < n) add(early[j], group + j * groups);
+        for (int j = 0; j < EARLY; ++j)
+            if (group + j * groups < n) add(early[j], group + j * groups);
 #pragma unroll 8
-    for (int k = group + EARLY * groups; k < n; k += groups) add(part(k), k);
-    if (groups > 1) {
-        sums[group][threadIdx.x] = o;
-        __syncthreads();
-        if (group > 0) return;
-        for (int k = 1; k < groups; ++k) {                             // in order: the same result every time
-            const float4 v = sums[k][threadIdx.x];
-            o.x += v.x;
-            o.y += v.y;
-            o.z += v.z;
-            o.w += v.w;
-        }
-    }
-    const float v[4] = {o.x, o.y, o.z, o.w};
+        for (int k = group + EARLY * groups; k < n; k += groups) add(part(k, d), k);
+        if (c + 1 < chunks)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (row + j >= live) break;
-        const size_t at = (size_t)(row + j) * D + d;
-        if (F32) ((float *)a.out)[at] = v[j] * inv[j];
-        else ((__nv_bfloat16 *)a.out)[at] = __float2bfloat16_rn(v[j] * inv[j]);
+            for (int j = 0; j < EARLY; ++j)
+                early[j] = group + j * groups < n ? part(group + j * groups, d + 128) : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (groups > 1) {
+            sums[group][threadIdx.x] = o;
+            __syncthreads();
+            if (group == 0)
+                for (int k = 1; k < groups; ++k) {                     // in order: the same result every time
+                    const float4 v = sums[k][threadIdx.x];
+                    o.x += v.x;
+                    o.y += v.y;
+                    o.z += v.z;
+                    o.w += v.w;
+                }
+            __syncthreads();
+        }
+        if (group > 0) continue;
+        const float v[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (row + j >= live) break;
+            const size_t at = (size_t)(row + j) * D + d;
+            if (F32) ((float *)a.out)[at] = v[j] * inv[j];
+            else ((__nv_bfloat16 *)a.out)[at] = __float2bfloat16_rn(v[j] * inv[j]);
+        }
     }
 }
 
 constexpr int SLOTS = 2 * CTAS;
 
 struct Layout {
-    size_t o, ml, prefix, starts, bytes;
+    size_t o, ml, shared, bytes;
 };
 constexpr Layout layout()
 {
     Layout l = {};
     l.ml = sizeof(float) * (size_t)SLOTS * RT * D;
-    l.prefix = l.ml + sizeof(float2) * (size_t)SLOTS * RT;
-    l.starts = l.prefix + sizeof(int32_t) * (MAX_SPLIT_TILES + 1);
-    l.bytes = (l.starts + sizeof(int32_t) * CTAS + 255) & ~(size_t)255;
+    l.shared = l.ml + sizeof(float2) * (size_t)SLOTS * RT;
+    l.bytes = (l.shared + sizeof(int4) * CTAS + 255) & ~(size_t)255;
     return l;
 }
 
@@ -1057,17 +1086,27 @@ cudaError_t launch_variant(const CUtensorMap &map_q, const CUtensorMap &map_k, c
     }
     if (e != cudaSuccess || DEAL != SHARED) return e;
     LaunchScope scope(-1, st);
-    // about 8 parts to a group of threads, if every SM works on the same few row tiles
-    const int groups = std::max(1, std::min(JOIN_GROUPS, grid / (8 * a.tiles)));
-    return launch_pdl(prompt_join_kernel<SPLIT_P>, dim3(a.tiles * (RT / 4), CHUNKS), dim3(128, groups), 0, st, a);
+    // Few row tiles have many parts each: 148 for one token over 131072
+    // latents, joined in 45 us in all by 8 groups (71 by one); 32 tokens'
+    // about 5, for which one group is best (89 us, 118 with 8).
+    const int tiles = std::min(a.tiles, CTAS - 1), groups = std::max(1, std::min(JOIN_GROUPS, grid / (8 * a.tiles)));
+    const int chunks = tiles <= CTAS / 3 ? 1 : CHUNKS;                 // a wave or two of CTAs, most with nothing to do
+    return launch_pdl(prompt_join_kernel<SPLIT_P>, dim3(tiles * (RT / 4), CHUNKS / chunks), dim3(128, groups), 0, st, a, chunks);
+}
+
+// Whole row tiles, at worst the longest ones on one SM, take about as long as
+// planning and joining shared ones would.
+bool few_keys(int64_t tiles, int64_t n_k, int window)
+{
+    return (tiles + CTAS - 1) / CTAS * n_k <= 10 * KT || (window > 0 && window <= 4 * KT);
 }
 
 }  // namespace
 
 size_t prompt_workspace_bytes(int64_t n_q, int heads, int64_t n_k)
 {
-    // one key tile at most, or row tiles enough for every SM: nothing is shared
-    return n_k <= KT || row_tiles(n_q, heads) > MAX_SPLIT_TILES ? 256 : layout().bytes;
+    const int64_t tiles = row_tiles(n_q, heads);
+    return few_keys(tiles, n_k, 0) || tiles > MAX_SPLIT_TILES ? 256 : layout().bytes;
 }
 
 cudaError_t launch_prompt_attend(const PromptArgs &p, cudaStream_t st)
@@ -1090,16 +1129,21 @@ cudaError_t launch_prompt_attend(const PromptArgs &p, cudaStream_t st)
     a.error = p.error;
     a.part_o = (float *)((char *)p.ws + l.o);
     a.part_ml = (float2 *)((char *)p.ws + l.ml);
-    a.prefix = (int32_t *)((char *)p.ws + l.prefix);
-    a.starts = (int32_t *)((char *)p.ws + l.starts);
+    a.shared = (int4 *)((char *)p.ws + l.shared);
     CUtensorMap map_q, map_k, map_out;
     // Without keys the latents' map covers a row of q that every mask leaves out.
     if (!make_map(&map_q, p.q, (int64_t)p.n_q * p.heads, D, RT, 8) ||
         !make_map(&map_out, p.out, (int64_t)p.n_q * p.heads, D, RT, 1) ||        // f32 outputs do not use it
         !make_map(&map_k, p.n_k ? p.lat : p.q, p.n_k ? p.n_k : 1, p.n_k ? p.lat_stride : D, KT, 2))
         return cudaErrorInvalidValue;
+    // Sharing evens out few rows or ragged pasts (50 tokens after 4000: 57 us
+    // against 88 whole; 32 tokens with pasts of 32 to 16384: 34 against 244),
+    // but plans and joins (100 tokens after 1000: 43 against 30); many row
+    // tiles are even enough dealt round robin (800 tokens after 20000: 2.38
+    // ms shared, 2.45 whole).  Sliding: one token 9.5 us either way, 4000
+    // tokens 110 against 120 us.
     const bool sliding = p.window > 0 && p.window <= KT && p.heads % RT == 0;
-    if (sliding || p.n_k <= KT || a.tiles > MAX_SPLIT_TILES) {         // one key tile each, or enough for every SM
+    if (sliding || few_keys(a.tiles, p.n_k, p.window) || a.tiles > MAX_SPLIT_TILES) {
         const int grid = std::min(a.tiles, CTAS);
         if (sliding)
             return p.out_is_fp32 ? launch_variant<true, SLIDING>(map_q, map_k, map_out, a, grid, st)

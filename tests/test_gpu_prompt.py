@@ -141,7 +141,9 @@ def test_sharp_and_flat_weights():
     for scale in (0.0, -SCALE, 2.0):
         out, lse, _ = _call(q, lat, cu_q, cu_k, 0, True, scale=scale)
         _check(out, lse, _ref(q, lat, n - 4, 0, scale))
-    assert csa2.csa2_prompt_workspace_bytes(4, 64, 128) < csa2.csa2_prompt_workspace_bytes(4, 64, 129)
+    # few keys need next to no workspace, many rows neither
+    many = csa2.csa2_prompt_workspace_bytes(4, 64, 100000)
+    assert max(csa2.csa2_prompt_workspace_bytes(4, 64, 128), csa2.csa2_prompt_workspace_bytes(5000, 64, 100000)) < many
 
 
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
