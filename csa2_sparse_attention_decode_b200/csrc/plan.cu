@@ -25,28 +25,38 @@ constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
 constexpr int TOK_PER_THREAD = 4;
 
-// Exclusive prefix sum of v over the CTA's threads; total gets the sum.
-// `red` is reused by the next call: two barriers keep the calls apart.
-__device__ __forceinline__ int64_t block_exclusive(int64_t v, int64_t *red, int64_t &total)
+// Exclusive prefix sums of two values over the CTA's threads; total gets their
+// sums.  `red` is reused by the next call: two barriers keep the calls apart.
+struct Pair {
+    int64_t a, b;
+};
+__device__ __forceinline__ Pair block_exclusive(Pair v, Pair *red, Pair &total)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t x = v;
+    Pair x = v;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int64_t y = __shfl_up_sync(~0u, x, d);
-        if (lane >= d) x += y;
+        const int64_t a = __shfl_up_sync(~0u, x.a, d), b = __shfl_up_sync(~0u, x.b, d);
+        if (lane >= d) {
+            x.a += a;
+            x.b += b;
+        }
     }
     __syncthreads();
     if (lane == 31) red[warp] = x;
     __syncthreads();
-    int64_t before = 0, sum = 0;
+    Pair before = {0, 0}, sum = {0, 0};
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
-        if (w < warp) before += red[w];
-        sum += red[w];
+        if (w < warp) {
+            before.a += red[w].a;
+            before.b += red[w].b;
+        }
+        sum.a += red[w].a;
+        sum.b += red[w].b;
     }
     total = sum;
-    return before + x - v;
+    return {before.a + x.a - v.a, before.b + x.b - v.b};
 }
 
 // Last index i of a[0 .. n] with a[i] <= x; a is non-decreasing, a[0] <= x < a[n].
@@ -71,15 +81,11 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(PlanArgs a)
     const int B = a.batch;
     int *cu = sh, *taken = cu + B + 1, *rel = taken + B + 1;           // prefix sums
     int *past = rel + B + 1, *owned = past + B, *ratio = owned + B;
-    __shared__ int64_t red[WARPS];
+    __shared__ Pair red[WARPS];
     grid_dependency_wait();
     allow_dependents();
     const bool first = blockIdx.x == 0;                                // reports and writes what is there once
-    int n_free = *a.n_free;
-    if (n_free < 0 || n_free > a.n_pages) {
-        if (first && threadIdx.x == 0) set_error(a.error, CSA2_DEV_BAD_REQUEST);
-        n_free = max(0, min(n_free, a.n_pages));
-    }
+    const int n_free_in = *a.n_free, n_free = max(0, min(n_free_in, a.n_pages));
 
     // Each thread owns `per` consecutive requests, so one block scan of the
     // threads' sums gives every request its offset.  Until the last scan cu
@@ -87,7 +93,8 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(PlanArgs a)
     // bad data, or one the token rows or the stack cannot serve, has neither.
     const int per = (B + THREADS - 1) / THREADS;
     const int b0 = min(B, (int)threadIdx.x * per), b1 = min(B, b0 + per);
-    int64_t s_tok = 0, s_rel = 0, total;
+    int64_t s_tok = 0, s_rel = 0;
+    Pair total;
     for (int b = b0; b < b1; ++b) {
         const int t = a.n_tokens[b], m = a.m[b];
         int64_t nw = a.n_new[b];
@@ -108,14 +115,14 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(PlanArgs a)
         s_tok += cu[b];
         s_rel += rel[b];
     }
-    const int64_t rel0 = block_exclusive(s_rel, red, total);
-    int64_t top = n_free + total;
+    if (n_free != n_free_in && first && threadIdx.x == 0) set_error(a.error, CSA2_DEV_BAD_REQUEST);
+    const Pair start = block_exclusive({s_rel, s_tok}, red, total);
+    int64_t top = n_free + total.a;
     if (top > a.n_pages) {                                             // more pages than exist: a corrupt table
         if (first && threadIdx.x == 0) set_error(a.error, CSA2_DEV_CAPACITY);
         top = a.n_pages;
     }
-    int64_t at = block_exclusive(s_tok, red, total);
-    int64_t s_get = 0;
+    int64_t at = start.b, s_get = 0;
     for (int b = b0; b < b1; ++b) {                                    // token rows: served in order while they last
         at += cu[b];
         if (cu[b] > 0 && at > a.max_new) {
@@ -124,7 +131,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(PlanArgs a)
         }
         s_get += taken[b];
     }
-    at = block_exclusive(s_get, red, total);
+    at = block_exclusive({s_get, 0}, red, total).a;
     s_tok = s_get = 0;
     for (int b = b0; b < b1; ++b) {                                    // pages: likewise
         at += taken[b];
@@ -135,9 +142,9 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(PlanArgs a)
         s_tok += cu[b];
         s_get += taken[b];
     }
-    int64_t n_tok, n_get;
-    int64_t at_tok = block_exclusive(s_tok, red, n_tok), at_get = block_exclusive(s_get, red, n_get);
-    int64_t at_rel = rel0;
+    const Pair granted = block_exclusive({s_tok, s_get}, red, total);
+    const int64_t n_tok = total.a, n_get = total.b;
+    int64_t at_tok = granted.a, at_get = granted.b, at_rel = start.a;
     for (int b = b0; b < b1; ++b) {
         const int x = cu[b], y = taken[b], z = rel[b];
         cu[b] = (int)at_tok;
@@ -171,13 +178,15 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(PlanArgs a)
         return pid;
     };
 
-    const int gt = blockIdx.x * THREADS + threadIdx.x, threads = gridDim.x * THREADS;
-    for (int k = gt; k < rel[B]; k += threads) {                       // released pages onto the stack
+    // Pages from the last thread down, tokens from the first up: in a small
+    // step their loads do not wait for one another.
+    const int gt = blockIdx.x * THREADS + threadIdx.x, threads = gridDim.x * THREADS, down = threads - 1 - gt;
+    for (int k = down; k < rel[B]; k += threads) {                     // released pages onto the stack
         const int r = segment_of(rel, B, k);
         const int need = owned[r] - (rel[r + 1] - rel[r]);
         a.free_pages[n_free + k] = a.page_table[(size_t)r * a.max_pages + need + (k - rel[r])];
     }
-    for (int k = gt; k < taken[B]; k += threads) {                     // new pages into the tables
+    for (int k = down; k < taken[B]; k += threads) {                   // new pages into the tables
         const int r = segment_of(taken, B, k);
         a.page_table[(size_t)r * a.max_pages + owned[r] + (k - taken[r])] = stack_page((int)top - 1 - k);
     }
