@@ -10,8 +10,10 @@
 // read once.  A cluster of CTAs shares a request's row: every warp sums a
 // contiguous piece, the sums meet over distributed shared memory, and only
 // the warp whose piece holds the drawn index reads it again, from L2.  Sums
-// are fp64 (of fp32 differences that are exact there): over 10^5 terms fp32
-// sums would move the borders between tokens by more than a token's weight.
+// are fp64 over groups of 16 weights that are added as a tree in fp32: a group
+// is off by at most 2^-22 of itself, which moves a border between two tokens
+// by some 10^-9 of the total; fp64 throughout, with its conversions, took
+// twice the time, and fp32 throughout would move borders by whole tokens.
 // 64 requests x 131072 tokens: 24 us, 2.8 TB/s; what is left is latency: the
 // drafts' probabilities, then the row, then the sums, then the index, each
 // waits for the one before.
@@ -41,17 +43,17 @@ struct Weights {
     const float *p, *q;                        // q null: the drafter named token x for certain
     int x;
     bool residual;
-    __device__ __forceinline__ double of(float pv, float qv) const
+    __device__ __forceinline__ float of(float pv, float qv) const
     {
-        if (!residual) return pv > 0.0f ? (double)pv : 0.0;
-        return pv > qv ? (double)pv - (double)qv : 0.0;
+        if (!residual) return pv > 0.0f ? pv : 0.0f;
+        return pv > qv ? pv - qv : 0.0f;
     }
     __device__ __forceinline__ float draft(int v) const { return q ? q[v] : (v == x ? 1.0f : 0.0f); }
-    __device__ __forceinline__ double operator()(int v) const { return of(p[v], residual ? draft(v) : 0.0f); }
+    __device__ __forceinline__ float operator()(int v) const { return of(p[v], residual ? draft(v) : 0.0f); }
 };
 
 // Lanes i and i + 16 get the sum of the warp's i-th values.
-__device__ __forceinline__ double group_sums(double (&v)[BLOCK])
+__device__ __forceinline__ float group_sums(float (&v)[BLOCK])
 {
     const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -61,19 +63,20 @@ __device__ __forceinline__ double group_sums(double (&v)[BLOCK])
         const bool up = lane & d;
 #pragma unroll
         for (int i = 0; i < d; ++i) {
-            const double keep = up ? v[i + d] : v[i], send = up ? v[i] : v[i + d];
+            const float keep = up ? v[i + d] : v[i], send = up ? v[i] : v[i + d];
             v[i] = keep + __shfl_xor_sync(~0u, send, d);
         }
     }
     return v[0];
 }
 
-__device__ __forceinline__ double inclusive(double v)
+template <class T>
+__device__ __forceinline__ T inclusive(T v)
 {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const double y = __shfl_up_sync(~0u, v, d);
+        const T y = __shfl_up_sync(~0u, v, d);
         if (lane >= d) v += y;
     }
     return v;
@@ -88,22 +91,23 @@ __device__ __forceinline__ int search(const Weights &w, int v0, int v1, double c
     const int lane = threadIdx.x & 31;
     int last = v0;
     for (int v = v0; v < v1; v += 32 * BLOCK) {
-        double x[BLOCK];
+        float x[BLOCK];
 #pragma unroll
         for (int i = 0; i < BLOCK; ++i) {
             const int j = v + 32 * i + lane;
-            x[i] = j < v1 ? w(j) : 0.0;
-            if (x[i] > 0.0) last = j;
+            x[i] = j < v1 ? w(j) : 0.0f;
+            if (x[i] > 0.0f) last = j;
         }
-        const double all = group_sums(x), sum = lane < BLOCK ? all : 0.0;      // of groups, one a lane
+        const float all = group_sums(x);                               // of groups, one a lane
+        const double sum = lane < BLOCK ? (double)all : 0.0;
         const double upto = inclusive(sum);
         const unsigned over = __ballot_sync(~0u, c + upto > mark && sum > 0.0);
         if (over) {
             const int group = __ffs(over) - 1;
             const double start = c + __shfl_sync(~0u, upto - sum, group);
             const int j = v + 32 * group + lane;
-            const double y = j < v1 ? w(j) : 0.0, run = inclusive(y);
-            const unsigned hit = __ballot_sync(~0u, start + run > mark && y > 0.0), any = __ballot_sync(~0u, y > 0.0);
+            const float y = j < v1 ? w(j) : 0.0f, run = inclusive(y);
+            const unsigned hit = __ballot_sync(~0u, start + (double)run > mark && y > 0.0f), any = __ballot_sync(~0u, y > 0.0f);
             return v + 32 * group + (hit ? __ffs(hit) - 1 : 31 - __clz(any));
         }
         c += __shfl_sync(~0u, upto, 31);
@@ -173,7 +177,12 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(VerifyArgs a)
                     qv[i] = w.residual && j < e ? w.draft(j) : 0.0f;
                 }
 #pragma unroll
-                for (int i = 0; i < BLOCK; ++i) s += w.of(pv[i], qv[i]);
+                for (int i = 0; i < BLOCK; ++i) pv[i] = w.of(pv[i], qv[i]);
+#pragma unroll
+                for (int i = BLOCK / 2; i > 0; i >>= 1)
+#pragma unroll
+                    for (int j = 0; j < i; ++j) pv[j] += pv[j + i];
+                s += pv[0];
             }
             s = warp_sum(s);
             if (lane == r) sums = s;
