@@ -8,7 +8,7 @@
 // batch (released pages, taken pages, granted tokens) place everything.
 //
 // Bound: 12 bytes written per new token (request, position, slot); a decode
-// step's 64 tokens are pure latency (5.4 us, of them 2.5 the launch).  So one launch does it all, and no CTA
+// step's 64 tokens are pure latency (4.8 us, of them 2.5 the launch).  So one launch does it all, and no CTA
 // waits for another: each repeats the prefix sums (two loads' latency and
 // three block scans) and then takes its share of the tokens.  That works
 // because nothing a CTA reads is written in the same launch: a taken page is
@@ -260,10 +260,10 @@ cudaError_t launch_plan(const PlanArgs &a, cudaStream_t st)
         });
     if (e != cudaSuccess) return e;
     // 1024 tokens a CTA; and, since releases can be many pages whatever the
-    // tokens (300 requests, a quarter of them dropping tokens: 9.5 us with two
-    // CTAs, 8.4 with 8 or more), 16 requests a CTA.  More than two CTAs an SM
-    // only repeat the prefix sums (295000 tokens: 6.2 us with 296, 8.8 with
-    // 592, 14 with 37).
+    // tokens (300 requests, a quarter of them dropping tokens: 8.2 us with two
+    // CTAs, 7.1 with 8 or more), 16 requests a CTA.  More than two CTAs an SM
+    // only repeat the prefix sums (295000 tokens: 5.4 us with 296, 7.3 with
+    // 592, 13 with 37).
     const int64_t want = std::max(((int64_t)a.max_new + THREADS * TOK_PER_THREAD - 1) / (THREADS * TOK_PER_THREAD),
                                   ((int64_t)a.batch + 15) / 16);
     const int grid = (int)std::min<int64_t>(want, 2 * 148);

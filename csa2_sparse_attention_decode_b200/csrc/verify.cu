@@ -14,7 +14,7 @@
 // is off by at most 2^-22 of itself, which moves a border between two tokens
 // by some 10^-9 of the total; fp64 throughout, with its conversions, took
 // twice the time, and fp32 throughout would move borders by whole tokens.
-// 64 requests x 131072 tokens: 24 us, 2.8 TB/s; what is left is latency: the
+// 64 requests x 131072 tokens: 18 us, 3.8 TB/s; what is left is latency: the
 // drafts' probabilities, then the row, then the sums, then the index, each
 // waits for the one before.
 #include "common.cuh"
@@ -246,9 +246,9 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(VerifyArgs a)
 cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t st)
 {
     // As many CTAs to a request as can all be at work (two on each of 148
-    // SMs), and no more than its row has blocks for.  64 rows of 131072: 24 us
-    // with 4, 30 with 2 or 8; 8 of 100003: 12 with 8, 16 with 4; 2 of 16384:
-    // 9.1 with 2, 9.5 with 8.
+    // SMs), and no more than its row has blocks for.  64 rows of 131072: 17.5
+    // us with 4, 19.8 with 2, 23.5 with 8; 8 of 100003: 10.0 with 8, 12.0 with
+    // 4; 2 of 16384: 8.2 with 2 or more, 9.0 with 1.
     int nc = MAX_CLUSTER;
     while (nc > 1 && ((int64_t)a.batch * nc > 2 * 148 || a.vocab < nc * WARPS * 32 * BLOCK / 2)) nc /= 2;
     LaunchScope scope(-1, st);

@@ -337,7 +337,7 @@ csa2_status csa2_combine(int32_t n_parts, const float *const *o_parts, const flo
  * max(p_n - q_n, 0) if draft n was refused (from p_n where that is zero
  * everywhere), else from p_n: the first index whose cumulative weight
  * exceeds u[b][max_draft] times the total, weights of zero, negative and NaN
- * being never drawn; sums are fp64.
+ * being never drawn; 16 weights are added in fp32, those sums in fp64.
  *   target [batch][max_draft + 1][vocab] f32: p_i, need not sum to one
  *   probs  [batch][max_draft][vocab] f32: q_i, or NULL for a drafter that
  *          names its token without probabilities (q_i = 1 at that token)
@@ -430,7 +430,8 @@ csa2_status csa2_norm_rope(int32_t n, int32_t dim, int32_t heads, const uint16_t
  *   ws: at least csa2_prompt_workspace_bytes(), 256-byte aligned; its
  *          contents are not kept.  Calls that may overlap need one each.
  * Tokens from cu_q[batch] on are left as they were.  A latent that is not
- * finite turns the queries that see it to NaN and no other.  cu_q or cu_k
+ * finite leaves the queries that see it no finite output in its channel (a
+ * NaN: in none) and changes no other query's.  cu_q or cu_k
  * that fall or pass n_q or n_k set CSA2_DEV_BAD_REQUEST; nothing outside the
  * given arrays is read or written.  heads 1..128, n_q * heads < 2^31 - 64. */
 size_t csa2_prompt_workspace_bytes(int32_t n_q, int32_t heads, int32_t n_k);
