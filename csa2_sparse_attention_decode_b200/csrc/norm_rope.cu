@@ -42,6 +42,20 @@ __device__ __forceinline__ uint32_t pack2(float a, float b)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// Two fp32 products, or products and sums, in one instruction, each rounded as by itself.
+__device__ __forceinline__ void mul2(float &a0, float &a1, float b0, float b1)
+{
+    asm("{\n.reg .b64 x, y;\nmov.b64 x, {%0, %1};\nmov.b64 y, {%2, %3};\nmul.rn.f32x2 x, x, y;\nmov.b64 {%0, %1}, x;\n}\n"
+        : "+f"(a0), "+f"(a1)
+        : "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void square_add2(float &s0, float &s1, float b0, float b1)
+{
+    asm("{\n.reg .b64 x, y;\nmov.b64 x, {%0, %1};\nmov.b64 y, {%2, %3};\nfma.rn.f32x2 x, y, y, x;\nmov.b64 {%0, %1}, x;\n}\n"
+        : "+f"(s0), "+f"(s1)
+        : "f"(b0), "f"(b1));
+}
+
 // DIM channels a row.  A step is 1 KB of rows: a lane holds two 16-byte chunks
 // of one row.  With halves its second chunk is the first one's partner, `away`
 // chunks on, so that the rotation stays in the lane.
@@ -81,7 +95,7 @@ __device__ __forceinline__ void finish(const NormRopeArgs &a, const uint4 (&raw)
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum[k] += x[k][i] * x[k][i];
+            for (int i = 0; i < 8; i += 2) square_add2(sum[0], sum[1], x[k][i], x[k][i + 1]);
         sum[0] += sum[1];
 #pragma unroll
         for (int d = Shape<DIM>::LANES / 2; d > 0; d >>= 1) sum[0] += __shfl_xor_sync(~0u, sum[0], d);
@@ -89,7 +103,10 @@ __device__ __forceinline__ void finish(const NormRopeArgs &a, const uint4 (&raw)
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[k][i] = x[k][i] * inv * w[k][i];
+            for (int i = 0; i < 8; i += 2) {
+                mul2(x[k][i], x[k][i + 1], inv, inv);
+                mul2(x[k][i], x[k][i + 1], w[k][i], w[k][i + 1]);
+            }
     }
     if (a.rot_dim == 0) return;
     const int skip = (DIM - a.rot_dim) / 8;                            // chunks before the rotated range
