@@ -14,9 +14,9 @@
 // flight (two rows of 512 channels, four of 256, ...), takes a slice of a
 // token's rows with their weights in registers, and forms the token's sines
 // once for the slice, in its own shared memory.  8192 tokens x 65 rows of 512:
-// 198 us, 5.5 TB/s, 0.85 of the measured copy rate; 16381 tokens x 33 rows of
-// 128 in halves: 69 us, 4.1 TB/s (60 % of the issue slots: short rows have
-// more instructions a byte).
+// 195 us, 5.6 TB/s, 0.86 of the measured copy rate; 16381 tokens x 33 rows of
+// 128 in halves: 66 us, 4.3 TB/s (short rows have more instructions a byte;
+// products and sums in pairs took it there from 69).
 #include "common.cuh"
 #include "serve.cuh"
 
@@ -49,6 +49,13 @@ __device__ __forceinline__ void mul2(float &a0, float &a1, float b0, float b1)
         : "+f"(a0), "+f"(a1)
         : "f"(b0), "f"(b1));
 }
+__device__ __forceinline__ void multiply_add2(float &a0, float &a1, float b0, float b1, float c0, float c1)
+{
+    asm("{\n.reg .b64 x, y, z;\nmov.b64 x, {%0, %1};\nmov.b64 y, {%2, %3};\nmov.b64 z, {%4, %5};\nfma.rn.f32x2 x, x, y, z;\n"
+        "mov.b64 {%0, %1}, x;\n}\n"
+        : "+f"(a0), "+f"(a1)
+        : "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
 __device__ __forceinline__ void square_add2(float &s0, float &s1, float b0, float b1)
 {
     asm("{\n.reg .b64 x, y;\nmov.b64 x, {%0, %1};\nmov.b64 y, {%2, %3};\nfma.rn.f32x2 x, y, y, x;\nmov.b64 {%0, %1}, x;\n}\n"
@@ -66,20 +73,23 @@ struct Shape {
     static constexpr int ROWS = 32 / LANES;                            // of a step
 };
 
-// The cosine and sine of pair p lie so that lanes with neighbouring chunks read
-// neighbouring 16 bytes: two pairs in each, `per` pairs to a chunk.
-__device__ __forceinline__ int turn_at(int p, int per, int half) { return ((p % per / 2) * (half / per) + p / per) * 2 + (p & 1); }
+// The cosines and sines of two pairs (c, c, s, s) share 16 bytes, and lanes with
+// neighbouring chunks, `per` pairs each, read neighbouring ones: the cosine of
+// pair p is float turn_at(p), its sine two floats on.
+__device__ __forceinline__ int turn_at(int p, int per, int half) { return ((p % per / 2) * (half / per) + p / per) * 4 + (p & 1); }
 
 // A warp forms a token's cosines and sines.  Not inlined: its registers would
 // crowd out the rows in flight.
-__device__ __noinline__ void fill_turns(float2 *turn, const float *inv_freq, int half, int per, int pos, float sign)
+__device__ __noinline__ void fill_turns(float *turn, const float *inv_freq, int half, int per, int pos, float sign)
 {
     for (int i = threadIdx.x & 31; i < half; i += 32) {
         double t = (double)pos * (double)inv_freq[i] * 0.15915494309189535;            // 1 / 2 pi
         t -= rint(t);
         float sine, cosine;
         sincospif(2.0f * (float)t, &sine, &cosine);
-        turn[turn_at(i, per, half)] = make_float2(cosine, sign * sine);
+        float *at = turn + turn_at(i, per, half);
+        at[0] = cosine;
+        at[2] = sign * sine;
     }
 }
 
@@ -119,10 +129,10 @@ __device__ __forceinline__ void finish(const NormRopeArgs &a, const uint4 (&raw)
             for (int i = 0; i < 4; i += 2) {
                 const float4 v = turn[i / 2 * chunks + c[k] - skip];
                 const float a0 = x[k][2 * i], b0 = x[k][2 * i + 1], a1 = x[k][2 * i + 2], b1 = x[k][2 * i + 3];
-                x[k][2 * i] = a0 * v.x - b0 * v.y;
-                x[k][2 * i + 1] = a0 * v.y + b0 * v.x;
-                x[k][2 * i + 2] = a1 * v.z - b1 * v.w;
-                x[k][2 * i + 3] = a1 * v.w + b1 * v.z;
+                x[k][2 * i] = a0 * v.x - b0 * v.z;
+                x[k][2 * i + 1] = a0 * v.z + b0 * v.x;
+                x[k][2 * i + 2] = a1 * v.y - b1 * v.w;
+                x[k][2 * i + 3] = a1 * v.w + b1 * v.y;
             }
         }
     } else if (c[0] >= skip) {
@@ -130,11 +140,11 @@ __device__ __forceinline__ void finish(const NormRopeArgs &a, const uint4 (&raw)
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
             const float4 v = turn[i / 2 * chunks + c[0] - skip];
-            const float a0 = x[0][i], b0 = x[1][i], a1 = x[0][i + 1], b1 = x[1][i + 1];
-            x[0][i] = a0 * v.x - b0 * v.y;
-            x[1][i] = a0 * v.y + b0 * v.x;
-            x[0][i + 1] = a1 * v.z - b1 * v.w;
-            x[1][i + 1] = a1 * v.w + b1 * v.z;
+            float s0 = x[0][i], s1 = x[0][i + 1], t0 = x[1][i], t1 = x[1][i + 1];      // a s and -b s
+            mul2(s0, s1, v.z, v.w);
+            mul2(t0, t1, -v.z, -v.w);
+            multiply_add2(x[0][i], x[0][i + 1], v.x, v.y, t0, t1);
+            multiply_add2(x[1][i], x[1][i + 1], v.x, v.y, s0, s1);
         }
     }
 }
@@ -145,12 +155,12 @@ template <int DIM>
 __global__ void __launch_bounds__(THREADS, 4) norm_rope_kernel(NormRopeArgs a, int slices, int q_steps, int steps)
 {
     using S = Shape<DIM>;
-    extern __shared__ __align__(16) float2 turns[];                    // [WARPS][R/2] cosine, sine
+    extern __shared__ __align__(16) float turns[];                     // [WARPS][R] cosines and sines
     const int lane = threadIdx.x & 31, l = lane & (S::LANES - 1), sub = lane / S::LANES;
     const int half = a.rot_dim / 2, per = a.flags & CSA2_ROPE_HALVES ? 8 : 4;
     const int away = a.flags & CSA2_ROPE_HALVES && half ? half / 8 : S::LANES;
     const int c[2] = {(l / away * 2) * away + l % away, (l / away * 2 + 1) * away + l % away};
-    float2 *turn = turns + (threadIdx.x >> 5) * half;
+    float *turn = turns + (threadIdx.x >> 5) * a.rot_dim;
     grid_dependency_wait();
     allow_dependents();
 
@@ -231,7 +241,7 @@ cudaError_t launch_dim(const NormRopeArgs &a, cudaStream_t st)
     const int64_t blocks = ((int64_t)a.n * slices + WARPS - 1) / WARPS;
     LaunchScope scope(-1, st);
     return launch_pdl(norm_rope_kernel<DIM>, dim3((unsigned)std::min<int64_t>(blocks, RESIDENT / WARPS)), dim3(THREADS),
-                      sizeof(float2) * WARPS * (a.rot_dim / 2), st, a, slices, q_steps, steps);
+                      sizeof(float) * WARPS * a.rot_dim, st, a, slices, q_steps, steps);
 }
 
 }  // namespace
