@@ -16,8 +16,8 @@
 // would fill all of it with O alone.
 //
 // Running softmax.  m is a reference, not the maximum: it moves only when a
-// score passes it by 2^8, so the usual tile has no reduction over keys; the
-// weights stay below 2^8, and l and O are fp32.  The sums l stay in registers
+// score passes it by a factor 2^32, so the usual tile has no reduction over
+// keys; the weights stay below 2^32, and l and O are fp32.  The sums l stay in registers
 // per key slot and are reduced once per tile of rows.
 //
 // P is rounded to bf16 for the second product (relative 2^-9, below the bf16
@@ -678,7 +678,8 @@ __device__ void softmax(const Args &a, Misc *m, uint8_t *sm)
                     // A latent that is not finite gives no finite score at
                     // all.  A masked weight of zero would not keep it out of
                     // O, so it is cleared, and the rows that do see it become
-                    // NaN.
+                    // NaN.  (Queries that are not finite look the same, and
+                    // become NaN by themselves.)
                     const int key = key0 + ((row - g.turn) & (KT - 1));
                     float least = INFINITY;
 #pragma unroll
@@ -688,8 +689,22 @@ __device__ void softmax(const Args &a, Misc *m, uint8_t *sm)
                     if (soft_any(all)) {
                         bad_key[half * KT + row] = all;
                         soft_sync();
-                        const bool found = bad_key[row] && bad_key[KT + row];
+                        bool found = bad_key[row] && bad_key[KT + row];
                         soft_sync();
+                        if (DEAL == SLIDING) {                         // the ring goes on to tokens with other queries: look
+                            for (int c = 0; c < CHUNKS; ++c) mbar_try_wait(&m->k_full[c], unit & 1);        // long true: orders the loads
+                            uint32_t exponent = 0;                     // the largest ones of this half of the latent
+                            if (found)
+#pragma unroll 1
+                                for (int i = 0; i < 4 * K_SLAB; i += i % 128 < 124 ? 4 : K_SLAB - 124) {
+                                    const uint8_t *at = sm + K_OFF + 4 * half * K_SLAB + row * 128 + i;
+                                    exponent = __vmaxu2(exponent, *reinterpret_cast<const uint32_t *>(at) & 0x7f807f80u);
+                                }
+                            bad_key[half * KT + row] = (exponent & 0xffffu) == 0x7f80u || exponent >> 16 == 0x7f80u;
+                            soft_sync();
+                            found = bad_key[row] || bad_key[KT + row];
+                            soft_sync();
+                        }
                         if (DEAL == SLIDING && found && half == 0) atomicOr(&m->cleared[row >> 5], 1u << (row & 31));
                         poison |= found;
                         if (found)

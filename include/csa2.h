@@ -431,8 +431,8 @@ csa2_status csa2_norm_rope(int32_t n, int32_t dim, int32_t heads, const uint16_t
  *          contents are not kept.  Calls that may overlap need one each.
  * Tokens from cu_q[batch] on are left as they were.  A latent that is not
  * finite leaves the queries that see it no finite output in its channel (a
- * NaN: in none) and changes no other query's.  cu_q or cu_k
- * that fall or pass n_q or n_k set CSA2_DEV_BAD_REQUEST; nothing outside the
+ * NaN: in none) and changes no other query's, nor does a query that is not
+ * finite.  cu_q or cu_k that fall or pass n_q or n_k set CSA2_DEV_BAD_REQUEST; nothing outside the
  * given arrays is read or written.  heads 1..128, n_q * heads < 2^31 - 64. */
 size_t csa2_prompt_workspace_bytes(int32_t n_q, int32_t heads, int32_t n_k);
 csa2_status csa2_prompt_attend(int32_t batch, const int32_t *cu_q, const int32_t *cu_k, int32_t n_q, int32_t n_k,

@@ -206,6 +206,23 @@ def test_queries_that_are_not_finite_stay_alone():
     assert torch.equal(out[~hit], clean[~hit]) and out[hit].isnan().all()
 
 
+@pytest.mark.parametrize("heads", [64, 128])
+@pytest.mark.parametrize("window", [128, 100, 1])
+def test_queries_that_are_not_finite_leave_the_tokens_behind_them_alone(heads, window):
+    # runs of tokens that share a ring of latents: every score of a key may be NaN though its latent is not
+    n = 700
+    q, lat = _inputs(heads + window, [n], [n], heads)
+    clean, clean_lse, _ = _call(q, lat, _cu([n]), _cu([n]), window)
+    bad = q.clone()
+    hit = torch.zeros(n, heads, dtype=torch.bool, device="cuda")
+    for t in (0, 3, 64, 250, 251, 600):
+        bad[t, :64] = float("nan")
+        hit[t, :64] = True
+    out, lse, _ = _call(bad, lat, _cu([n]), _cu([n]), window)
+    assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse[~hit], clean_lse[~hit])
+    assert out[hit].isnan().all() and lse[hit].isnan().all()
+
+
 def test_bad_prefix_sums_are_reported():
     q, lat = _inputs(2, [100], [300], 24)
     i32 = dict(dtype=torch.int32, device="cuda")
