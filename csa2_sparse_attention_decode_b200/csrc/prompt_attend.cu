@@ -1014,7 +1014,7 @@ __global__ void __launch_bounds__(128 * JOIN_GROUPS) prompt_join_kernel(const Ar
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
         if (lane == 0) {
-            const bool none = top == -INFINITY;
+            const bool none = top == -INFINITY && sum == 0.0f;         // a NaN has seen keys
             inv[warp] = none ? 0.0f : 1.0f / sum;
             if (blockIdx.y == 0 && a.lse && row + warp < live)
                 a.lse[row + warp] = none ? -INFINITY : (top + log2f(sum)) * LN2;

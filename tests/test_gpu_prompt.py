@@ -223,6 +223,18 @@ def test_queries_that_are_not_finite_leave_the_tokens_behind_them_alone(heads, w
     assert out[hit].isnan().all() and lse[hit].isnan().all()
 
 
+def test_a_query_that_is_not_finite_over_shared_keys():
+    q, lat = _inputs(11, [2], [9000], 64)      # every SM has a part of each token
+    clean, clean_lse, _ = _call(q, lat, _cu([2]), _cu([9000]))
+    bad = q.clone()
+    bad[0] = float("nan")
+    bad[1, 5] = float("nan")
+    out, lse, _ = _call(bad, lat, _cu([2]), _cu([9000]))
+    hit = bad.isnan().any(-1)
+    assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse[~hit], clean_lse[~hit])
+    assert out[hit].isnan().all() and lse[hit].isnan().all()
+
+
 def test_bad_prefix_sums_are_reported():
     q, lat = _inputs(2, [100], [300], 24)
     i32 = dict(dtype=torch.int32, device="cuda")
