@@ -326,8 +326,9 @@ csa2_status csa2_combine(int32_t n_parts, const float *const *o_parts, const flo
  * csa2_plan_tokens gives the tokens that come their pages and slots,
  * csa2_norm_rope prepares queries, latents and indexer keys,
  * csa2_prompt_attend attends a prompt's tokens, csa2_prefill / csa2_append
- * write them and csa2_index / csa2_attend read them.  `error` is a device word as in csa2_cache (it may be the cache's).
- * Rows behind the last token are never written. */
+ * write them and csa2_index / csa2_attend read them.  `error` is a device
+ * word as in csa2_cache (it may be the cache's).  Rows behind the last token
+ * are never written. */
 
 /* Verification of drafted tokens: which drafts stay, and the token after
  * them, from given random numbers.  Request b has n_draft[b] (0..max_draft)
@@ -346,8 +347,8 @@ csa2_status csa2_combine(int32_t n_parts, const float *const *o_parts, const flo
  *   n_accepted [batch] i32; tokens [batch][max_draft + 1] i32: the kept
  *          drafts, the drawn token, then -1
  * max_draft 0..CSA2_MAX_DRAFT.  A drafted token outside the vocabulary is
- * refused (CSA2_DEV_BAD_INDEX); a row without positive finite weight gives
- * the last token (CSA2_DEV_BAD_REQUEST). */
+ * refused (CSA2_DEV_BAD_INDEX); a row whose weights have no positive
+ * finite total gives the last token (CSA2_DEV_BAD_REQUEST). */
 #define CSA2_MAX_DRAFT 31
 csa2_status csa2_verify(int32_t batch, int32_t max_draft, int32_t vocab, const float *target, const float *probs,
                         const int32_t *draft, const int32_t *n_draft, const float *u, int32_t *n_accepted,
