@@ -12,11 +12,10 @@
 // Bound: 4 bytes per element, read and written once.  A row stays in its
 // warp's registers, so nothing is read twice.  A warp has 2 KB of rows in
 // flight (two rows of 512 channels, four of 256, ...), takes a slice of a
-// token's rows with their weights in registers, and forms the token's sines
-// once for the slice, in its own shared memory.  8192 tokens x 65 rows of 512:
-// 195 us, 5.6 TB/s, 0.86 of the measured copy rate; 16381 tokens x 33 rows of
-// 128 in halves: 66 us, 4.3 TB/s (short rows have more instructions a byte;
-// products and sums in pairs took it there from 69).
+// token's rows, and forms the token's sines once for the slice, in its own
+// shared memory.  8192 tokens x 65 rows of 512: 186 us, 5.9 TB/s, 0.90 of the
+// measured copy rate; 16381 tokens x 33 rows of 128 in halves: 60 us, 4.7 TB/s
+// (short rows have more instructions a byte; two of fp32 at a time took 3 us off).
 #include "common.cuh"
 #include "serve.cuh"
 
@@ -63,9 +62,17 @@ __device__ __forceinline__ void square_add2(float &s0, float &s1, float b0, floa
         : "f"(b0), "f"(b1));
 }
 
+// A read that may pass the stores before it, but not the wait for the kernel
+// before this one.
+__device__ __forceinline__ float4 load_constant(const float *p)
+{
+    float4 v;
+    asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+    return v;
+}
+
 // DIM channels a row.  A step is 1 KB of rows: a lane holds two 16-byte chunks
-// of one row.  With halves its second chunk is the first one's partner, `away`
-// chunks on, so that the rotation stays in the lane.
+// of one row, l and l + LANES, so that a row's lanes read and write whole lines.
 template <int DIM>
 struct Shape {
     static constexpr int CHUNKS = DIM / 8;                             // of a row
@@ -93,10 +100,14 @@ __device__ __noinline__ void fill_turns(float *turn, const float *inv_freq, int 
     }
 }
 
-// Norm and rotation of one step: x holds chunks c[0] and c[1] of a row, w the weights there.
-template <int DIM>
-__device__ __forceinline__ void finish(const NormRopeArgs &a, const uint4 (&raw)[2], float (&x)[2][8], const float (&w)[2][8],
-                                       const float4 *turn, const int (&c)[2])
+// Norm and rotation of one step: x holds chunks l and l + LANES of a row, w the
+// weights there.  In halves a channel's partner lies R/2 on: in the lane's
+// other chunk where the whole row turns, else, in the row's second half, in
+// another lane.  (16381 tokens x 33 rows of 128: 60 us, 67 with 64 channels
+// turned.  Lanes that hold both chunks of any pair: 66 either way.)
+template <int DIM, bool HALVES>
+__device__ __forceinline__ void finish(const NormRopeArgs &a, const uint4 (&raw)[2], float (&x)[2][8], const float (&held)[2][8],
+                                       const float *weight, const float4 *turn, const int (&c)[2])
 {
     unpack8(raw[0], x[0]);
     unpack8(raw[1], x[1]);
@@ -113,14 +124,18 @@ __device__ __forceinline__ void finish(const NormRopeArgs &a, const uint4 (&raw)
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
+            for (int i = 0; i < 8; i += 4) {
+                const float4 w = HALVES ? make_float4(held[k][i], held[k][i + 1], held[k][i + 2], held[k][i + 3])
+                                        : load_constant(weight + 8 * c[k] + i);
                 mul2(x[k][i], x[k][i + 1], inv, inv);
-                mul2(x[k][i], x[k][i + 1], w[k][i], w[k][i + 1]);
+                mul2(x[k][i], x[k][i + 1], w.x, w.y);
+                mul2(x[k][i + 2], x[k][i + 3], inv, inv);
+                mul2(x[k][i + 2], x[k][i + 3], w.z, w.w);
             }
     }
     if (a.rot_dim == 0) return;
     const int skip = (DIM - a.rot_dim) / 8;                            // chunks before the rotated range
-    if (!(a.flags & CSA2_ROPE_HALVES)) {
+    if (!HALVES) {
         const int chunks = a.rot_dim / 8;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -135,38 +150,52 @@ __device__ __forceinline__ void finish(const NormRopeArgs &a, const uint4 (&raw)
                 x[k][2 * i + 3] = a1 * v.w + b1 * v.y;
             }
         }
-    } else if (c[0] >= skip) {
-        const int chunks = a.rot_dim / 16;
+    } else if (a.rot_dim == DIM) {
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-            const float4 v = turn[i / 2 * chunks + c[0] - skip];
+            const float4 v = turn[i / 2 * Shape<DIM>::LANES + c[0]];
             float s0 = x[0][i], s1 = x[0][i + 1], t0 = x[1][i], t1 = x[1][i + 1];      // a s and -b s
             mul2(s0, s1, v.z, v.w);
             mul2(t0, t1, -v.z, -v.w);
             multiply_add2(x[0][i], x[0][i + 1], v.x, v.y, t0, t1);
             multiply_add2(x[1][i], x[1][i + 1], v.x, v.y, s0, s1);
         }
+    } else {
+        const int chunks = a.rot_dim / 16, at = (c[1] - skip) & (chunks - 1);          // of half the range
+        const bool turns = c[1] >= skip;
+        const float sign = c[1] - skip < chunks ? -1.0f : 1.0f;
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            float t0 = __shfl_xor_sync(~0u, x[1][i], chunks), t1 = __shfl_xor_sync(~0u, x[1][i + 1], chunks);
+            if (!turns) continue;
+            const float4 v = turn[i / 2 * chunks + at];
+            mul2(t0, t1, sign * v.z, sign * v.w);
+            multiply_add2(x[1][i], x[1][i + 1], v.x, v.y, t0, t1);
+        }
     }
 }
 
 // `slices` warps share a token; a warp takes every slices-th of its steps,
 // queries first, then latents.
-template <int DIM>
+template <int DIM, bool HALVES>
 __global__ void __launch_bounds__(THREADS, 4) norm_rope_kernel(NormRopeArgs a, int slices, int q_steps, int steps)
 {
     using S = Shape<DIM>;
     extern __shared__ __align__(16) float turns[];                     // [WARPS][R] cosines and sines
     const int lane = threadIdx.x & 31, l = lane & (S::LANES - 1), sub = lane / S::LANES;
-    const int half = a.rot_dim / 2, per = a.flags & CSA2_ROPE_HALVES ? 8 : 4;
-    const int away = a.flags & CSA2_ROPE_HALVES && half ? half / 8 : S::LANES;
-    const int c[2] = {(l / away * 2) * away + l % away, (l / away * 2 + 1) * away + l % away};
+    const int half = a.rot_dim / 2, per = HALVES ? 8 : 4;
+    const int c[2] = {l, l + S::LANES};
     float *turn = turns + (threadIdx.x >> 5) * a.rot_dim;
     grid_dependency_wait();
     allow_dependents();
 
     const int n = a.n_valid ? max(0, min(a.n, *a.n_valid)) : a.n;
     const int64_t items = (int64_t)n * slices;
-    float w[2][8] = {};
+    // The weights: neighbours read them from L1 at each step, which leaves
+    // registers (8192 tokens x 65 rows of 512: 186 us, held 194; 64 tokens
+    // 4.3, held 4.1); halves, whose rotation fills the registers either way,
+    // hold them (16381 tokens x 33 rows of 128: 60 us, from L1 64).
+    float held[2][8] = {};
     int weights_of = -1;                                               // 1: of the queries, 0: of the latents
     for (int64_t item = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5); item < items; item += (int64_t)gridDim.x * WARPS) {
         const int token = (int)(item / slices), slice = (int)(item - (int64_t)token * slices);
@@ -185,14 +214,14 @@ __global__ void __launch_bounds__(THREADS, 4) norm_rope_kernel(NormRopeArgs a, i
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
                     raw[u][k] = live[u] ? *reinterpret_cast<const uint4 *>(src + h[u] * DIM + 8 * c[k]) : make_uint4(0, 0, 0, 0);
-            if (weights_of != (int)is_q && !(a.flags & CSA2_ROPE_NO_NORM)) {
+            if (HALVES && weights_of != (int)is_q && !(a.flags & CSA2_ROPE_NO_NORM)) {
                 weights_of = is_q;
                 const float *ws = is_q ? a.q_weight : a.k_weight;
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const float4 wa = *reinterpret_cast<const float4 *>(ws + 8 * c[k]), wb = *reinterpret_cast<const float4 *>(ws + 8 * c[k] + 4);
-                    w[k][0] = wa.x, w[k][1] = wa.y, w[k][2] = wa.z, w[k][3] = wa.w;
-                    w[k][4] = wb.x, w[k][5] = wb.y, w[k][6] = wb.z, w[k][7] = wb.w;
+                    held[k][0] = wa.x, held[k][1] = wa.y, held[k][2] = wa.z, held[k][3] = wa.w;
+                    held[k][4] = wb.x, held[k][5] = wb.y, held[k][6] = wb.z, held[k][7] = wb.w;
                 }
             }
             if (!turned) {                                             // while the rows are on their way
@@ -206,7 +235,7 @@ __global__ void __launch_bounds__(THREADS, 4) norm_rope_kernel(NormRopeArgs a, i
             for (int u = 0; u < 2; ++u) {
                 if (u == 1 && !two) break;
                 float x[2][8];
-                finish<DIM>(a, raw[u], x, w, reinterpret_cast<const float4 *>(turn), c);
+                finish<DIM, HALVES>(a, raw[u], x, held, is_q ? a.q_weight : a.k_weight, reinterpret_cast<const float4 *>(turn), c);
                 if (!live[u]) continue;
                 const int64_t to = ((int64_t)token * heads + h[u]) * DIM;
 #pragma unroll
@@ -240,7 +269,7 @@ cudaError_t launch_dim(const NormRopeArgs &a, cudaStream_t st)
     if ((int64_t)a.n * slices < RESIDENT) slices = std::max(slices, std::min((steps + 1) / 2, RESIDENT / a.n));
     const int64_t blocks = ((int64_t)a.n * slices + WARPS - 1) / WARPS;
     LaunchScope scope(-1, st);
-    return launch_pdl(norm_rope_kernel<DIM>, dim3((unsigned)std::min<int64_t>(blocks, RESIDENT / WARPS)), dim3(THREADS),
+    return launch_pdl(a.flags & CSA2_ROPE_HALVES ? norm_rope_kernel<DIM, true> : norm_rope_kernel<DIM, false>, dim3((unsigned)std::min<int64_t>(blocks, RESIDENT / WARPS)), dim3(THREADS),
                       sizeof(float) * WARPS * a.rot_dim, st, a, slices, q_steps, steps);
 }
 
