@@ -13,7 +13,7 @@
 // warp's registers, so nothing is read twice.  A warp has 2 KB of rows in
 // flight (two rows of 512 channels, four of 256, ...), takes a slice of a
 // token's rows, and forms the token's sines once for the slice, in its own
-// shared memory.  8192 tokens x 65 rows of 512: 186 us, 5.9 TB/s, 0.90 of the
+// shared memory.  8192 tokens x 65 rows of 512: 187 us, 5.8 TB/s, 0.90 of the
 // measured copy rate; 16381 tokens x 33 rows of 128 in halves: 60 us, 4.7 TB/s
 // (short rows have more instructions a byte; two of fp32 at a time took 3 us off).
 #include "common.cuh"
@@ -262,9 +262,9 @@ cudaError_t launch_dim(const NormRopeArgs &a, cudaStream_t st)
     constexpr int ROWS = Shape<DIM>::ROWS;
     const int q_steps = (a.heads + ROWS - 1) / ROWS, steps = q_steps + (a.kv_heads + ROWS - 1) / ROWS;
     // A warp forms the sines for its slice of a token: 16 steps pay for them
-    // (8192 tokens x 65 rows of 512: 199 us in 4 slices, 207 in 1, 210 in 8).
+    // (8192 tokens x 65 rows of 512: 188 us in 4 slices, 202 in 1, 188 in 8).
     // Fewer tokens than warps: down to one pass of two steps each (64 tokens:
-    // 5.0 us in 32 slices, 8.6 in 8).
+    // 4.3 us in 32 slices, 7.4 in 8).
     int slices = std::max(1, steps / 16);
     if ((int64_t)a.n * slices < RESIDENT) slices = std::max(slices, std::min((steps + 1) / 2, RESIDENT / a.n));
     const int64_t blocks = ((int64_t)a.n * slices + WARPS - 1) / WARPS;

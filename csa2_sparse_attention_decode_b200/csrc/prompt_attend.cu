@@ -20,9 +20,9 @@
 // keys; the weights stay below 2^32, and l and O are fp32.  The sums l stay in registers
 // per key slot and are reduced once per tile of rows.
 //
-// P is rounded to bf16 for the second product (relative 2^-9, below the bf16
-// output's own step); for an fp32 output it is split into two bf16 parts
-// (2^-17) and the product taken twice.
+// P is rounded to bf16 for the second product (off by at most 2^-8 of itself,
+// as the bf16 output is); for an fp32 output it is split into two bf16 parts
+// (2^-16) and the product taken twice.
 //
 // Roles: eight warps do the softmax and the output, one warp plans the row
 // tiles and issues the TMA loads, one issues the MMAs.  A 128-dim chunk of
