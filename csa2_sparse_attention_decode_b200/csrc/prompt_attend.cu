@@ -537,7 +537,9 @@ __device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&r)[16])
                  : "r"(taddr));
 }
 
-// One warp has all of O that it stores in registers.
+// One warp has all of O that it stores in registers, and the factors it
+// scales them with: the softmax of the segment after next, which writes the
+// factors' other use, starts behind this.
 __device__ __forceinline__ void o_read(Misc *m)
 {
     fence_before_sync();
@@ -580,6 +582,9 @@ __device__ void store(const Args &a, Misc *m, uint8_t *stage, const CUtensorMap 
                 uint32_t o[32];
                 tmem_ld32(tb + RT * c + 32 * half, o);
                 tmem_ld_wait();
+                if (slot < 0)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fac[32 * half + j]);
                 if (ch == 2 * CHUNKS - 1) o_read(m);
                 if (slot >= 0) {
                     float *part = a.part_o + (size_t)slot * RT * D;
@@ -590,10 +595,13 @@ __device__ void store(const Args &a, Misc *m, uint8_t *stage, const CUtensorMap 
                     float *out = (float *)a.out + (size_t)(row0 + 32 * half) * D + d;
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        if (live[half] >> j & 1) out[(size_t)j * D] = __uint_as_float(o[j]) * fac[32 * half + j];
+                        if (live[half] >> j & 1) out[(size_t)j * D] = __uint_as_float(o[j]);
                 }
             }
         } else {
+            float2 f[8];                                               // of rows 8i + 2 (lane % 4) and the next
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = *reinterpret_cast<const float2 *>(fac + 8 * i + 2 * (lane & 3));
 #pragma unroll 1
             for (int c = 0; c < CHUNKS; ++c) {
                 uint32_t o[2][2][16];                                  // rows 0-31, 32-63; channels 0-15, 16-31 of the warp's
@@ -607,12 +615,11 @@ __device__ void store(const Args &a, Misc *m, uint8_t *stage, const CUtensorMap 
                 group_sync(group);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {                          // rows 8i .. 8i+7
-                    const float2 f = *reinterpret_cast<const float2 *>(fac + 8 * i + 2 * (lane & 3));
                     uint32_t v[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        v[k] = pack2(__uint_as_float(o[i >> 2][k >> 1][4 * (i & 3) + 2 * (k & 1)]) * f.x,
-                                     __uint_as_float(o[i >> 2][k >> 1][4 * (i & 3) + 2 * (k & 1) + 1]) * f.y);
+                        v[k] = pack2(__uint_as_float(o[i >> 2][k >> 1][4 * (i & 3) + 2 * (k & 1)]) * f[i].x,
+                                     __uint_as_float(o[i >> 2][k >> 1][4 * (i & 3) + 2 * (k & 1) + 1]) * f[i].y);
                     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
                                      smem_addr(box + put) + 1024 * i),
                                  "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
@@ -650,7 +657,7 @@ __device__ void softmax(const Args &a, Misc *m, uint8_t *sm)
     uint32_t unit = 0;
     for (uint32_t s = 0;; ++s) {
         const uint32_t r = s & 1;
-        if (soft_any(!wait(m, &m->seg_full[r], (s >> 1) & 1))) break;  // all eight warps leave, or none; fac, muse, P are free
+        if (soft_any(!wait(m, &m->seg_full[r], (s >> 1) & 1))) break;  // all eight warps leave, or none; muse and P are free
         const Segment g = m->seg[r];
         if (g.tile < 0) break;
         const int *lo = m->lo[r] + 32 * half, *hi = m->hi[r] + 32 * half;
@@ -661,6 +668,8 @@ __device__ void softmax(const Args &a, Misc *m, uint8_t *sm)
 
         int key0 = g.key0;
         for (int k = 0; k < g.n; ++k, ++unit, key0 = next_tile(g, m->lo[r], m->hi[r], key0)) {
+            // With the segment's first S the factors of two segments ago are free too: its products follow the last
+            // one's, which waited until the output warps had read O and those factors.
             wait(m, &m->s_full, unit & 1);                             // given up: finish the segment, then leave
             fence_after_sync();
             float x[32];

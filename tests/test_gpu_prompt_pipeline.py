@@ -1,0 +1,36 @@
+"""csa2_prompt_attend's pipeline of roles: what one row tile's output still needs is not overwritten by the row
+tiles behind it, whatever else loads the memory."""
+import pytest
+import torch
+
+from test_gpu_prompt import _call, _check, _cu, _inputs, _ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("heads,window", [(64, 128), (128, 100), (40, 200), (64, 0)])
+def test_factors_last_until_the_output_has_used_them(heads, window, f32):
+    # Two tokens of flat weights, then two of sharp ones, and so on: the sums that the rows are divided by differ
+    # by up to a hundred times from one row tile to the next but one.  Copies on other streams hold back the stores.
+    n = 1500
+    q, lat = _inputs(heads, [n], [n], heads)
+    q = q * torch.where(torch.arange(n, device="cuda") % 4 < 2, 0.0, 4.0).to(q.dtype)[:, None, None]
+    cu = _cu([n])
+    busy = [torch.empty(2, 1 << 27, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    streams = [torch.cuda.Stream() for _ in busy]
+    torch.cuda.synchronize()
+    runs = []
+    for _ in range(6):
+        for s, b in zip(streams, busy):
+            with torch.cuda.stream(s):
+                for _ in range(4):
+                    b[0].copy_(b[1])
+        runs.append(_call(q, lat, cu, cu, window, f32))
+    torch.cuda.synchronize()
+    for out, lse, err in runs:
+        assert int(err) == 0 and torch.equal(out, runs[0][0]) and torch.equal(lse, runs[0][1])
+    out, lse, _ = runs[0]
+    for t in range(0, n, 250):
+        lo = max(0, t + 1 - window) if window else 0
+        _check(out[t:t + 250], lse[t:t + 250], _ref(q[t:t + 250], lat[lo:t + 250], t - lo, window), f"tokens from {t}")
