@@ -9,14 +9,14 @@
 // Bound: one row of `vocab` probabilities per request, two after a refusal,
 // read once.  A cluster of CTAs shares a request's row: every warp sums a
 // contiguous piece, the sums meet over distributed shared memory, and only
-// the warp whose piece holds the drawn index reads it again, from L2.  Sums
-// are fp64 over groups of 16 weights that are added as a tree in fp32: a group
-// is off by at most 2^-22 of itself, which moves a border between two tokens
-// by some 10^-9 of the total; fp64 throughout, with its conversions, took
-// twice the time, and fp32 throughout would move borders by whole tokens.
-// 64 requests x 131072 tokens: 18 us, 3.8 TB/s; what is left is latency: the
-// drafts' probabilities, then the row, then the sums, then the index, each
-// waits for the one before.
+// the warp whose piece holds the drawn index reads it again, from L2.  A
+// lane adds 16 weights at a time as a tree of fp32 sums that keeps what each
+// addition rounds off, in fp32 too: off by at most 2^-42 of the 16 (low parts
+// of 5 x 2^-24, 8 roundings).  All further sums are fp64.  With every weight
+// converted to fp64 instead 64 requests x 131072 tokens take 19.0 us: a warp
+// converts 32 values in 16 cycles.  As it is 17.3 us, 51 MB in 2.9 TB/s; what
+// is left is latency: the drafts' probabilities, then the row, then the sums,
+// then the index, each waits for the one before.
 #include "common.cuh"
 #include "serve.cuh"
 
@@ -38,45 +38,33 @@ __device__ __forceinline__ double warp_sum(double v)
     return v;
 }
 
+// What t = a + b, rounded, leaves of the exact sum (Knuth's two-sum).
+__device__ __forceinline__ float lost(float a, float b, float t)
+{
+    const float z = t - a;
+    return (a - (t - z)) + (b - z);
+}
+
 // Weight of token v: the target's probability, or what the drafter's leaves of it.
 struct Weights {
     const float *p, *q;                        // q null: the drafter named token x for certain
     int x;
     bool residual;
-    __device__ __forceinline__ float of(float pv, float qv) const
+    __device__ __forceinline__ double of(float pv, float qv) const     // exact
     {
-        if (!residual) return pv > 0.0f ? pv : 0.0f;
-        return pv > qv ? pv - qv : 0.0f;
+        if (!residual) return pv > 0.0f ? (double)pv : 0.0;
+        return pv > qv ? (double)pv - (double)qv : 0.0;
     }
     __device__ __forceinline__ float draft(int v) const { return q ? q[v] : (v == x ? 1.0f : 0.0f); }
-    __device__ __forceinline__ float operator()(int v) const { return of(p[v], residual ? draft(v) : 0.0f); }
+    __device__ __forceinline__ double operator()(int v) const { return of(p[v], residual ? draft(v) : 0.0f); }
 };
 
-// Lanes i and i + 16 get the sum of the warp's i-th values.
-__device__ __forceinline__ float group_sums(float (&v)[BLOCK])
-{
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int i = 0; i < BLOCK; ++i) v[i] += __shfl_xor_sync(~0u, v[i], 16);
-#pragma unroll
-    for (int d = BLOCK / 2; d > 0; d >>= 1) {
-        const bool up = lane & d;
-#pragma unroll
-        for (int i = 0; i < d; ++i) {
-            const float keep = up ? v[i + d] : v[i], send = up ? v[i] : v[i + d];
-            v[i] = keep + __shfl_xor_sync(~0u, send, d);
-        }
-    }
-    return v[0];
-}
-
-template <class T>
-__device__ __forceinline__ T inclusive(T v)
+__device__ __forceinline__ double inclusive(double v)
 {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const T y = __shfl_up_sync(~0u, v, d);
+        const double y = __shfl_up_sync(~0u, v, d);
         if (lane >= d) v += y;
     }
     return v;
@@ -84,35 +72,57 @@ __device__ __forceinline__ T inclusive(T v)
 
 // First index in [v0, v1) whose cumulative weight, from `c` on, passes the
 // mark; where rounding leaves it a last bit short, the last with any weight.
-// 16 groups of 32 at a time: one round of loads, then sums of groups, then
-// the one group that holds the index.
-__device__ __forceinline__ int search(const Weights &w, int v0, int v1, double c, double mark)
+// 512 weights at a time: read side by side, then through shared memory to
+// lanes of 16 consecutive ones each: the lane that holds the index has it in
+// registers.
+struct Turn {
+    double w[BLOCK * (32 + 2)];                // 16 weights and a gap
+};
+__device__ __forceinline__ int search(const Weights &w, Turn &turn, int v0, int v1, double c, double mark)
 {
     const int lane = threadIdx.x & 31;
     int last = v0;
     for (int v = v0; v < v1; v += 32 * BLOCK) {
-        float x[BLOCK];
+        float p[BLOCK], q[BLOCK];                                      // all on their way before the first store
 #pragma unroll
         for (int i = 0; i < BLOCK; ++i) {
             const int j = v + 32 * i + lane;
-            x[i] = j < v1 ? w(j) : 0.0f;
-            if (x[i] > 0.0f) last = j;
+            p[i] = j < v1 ? w.p[j] : 0.0f;
+            q[i] = w.residual && j < v1 ? w.draft(j) : 0.0f;
         }
-        const float all = group_sums(x);                               // of groups, one a lane
-        const double sum = lane < BLOCK ? (double)all : 0.0;
+#pragma unroll
+        for (int i = 0; i < BLOCK; ++i) {
+            const int j = 32 * i + lane;
+            turn.w[j + j / BLOCK] = w.of(p[i], q[i]);
+        }
+        __syncwarp();
+        double x[BLOCK], sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < BLOCK; ++i) {
+            x[i] = turn.w[(BLOCK + 1) * lane + i];
+            sum += x[i];
+        }
+        __syncwarp();
         const double upto = inclusive(sum);
-        const unsigned over = __ballot_sync(~0u, c + upto > mark && sum > 0.0);
-        if (over) {
-            const int group = __ffs(over) - 1;
-            const double start = c + __shfl_sync(~0u, upto - sum, group);
-            const int j = v + 32 * group + lane;
-            const float y = j < v1 ? w(j) : 0.0f, run = inclusive(y);
-            const unsigned hit = __ballot_sync(~0u, start + (double)run > mark && y > 0.0f), any = __ballot_sync(~0u, y > 0.0f);
-            return v + 32 * group + (hit ? __ffs(hit) - 1 : 31 - __clz(any));
+        const unsigned over = __ballot_sync(~0u, c + upto > mark && sum > 0.0), some = __ballot_sync(~0u, sum > 0.0);
+        if (some) {                                                    // the lane that holds the index, or the last with any weight
+            const int holder = over ? __ffs(over) - 1 : 31 - __clz(some);
+            int at = -1, any = 0;
+            if (lane == holder) {
+                double run = c + (upto - sum);
+#pragma unroll
+                for (int i = 0; i < BLOCK; ++i) {
+                    run += x[i];
+                    if (x[i] > 0.0) any = i;
+                    if (x[i] > 0.0 && at < 0 && run > mark) at = i;
+                }
+            }
+            last = v + BLOCK * holder + __shfl_sync(~0u, over && at >= 0 ? at : any, holder);
+            if (over) return last;
         }
         c += __shfl_sync(~0u, upto, 31);
     }
-    return __reduce_max_sync(~0u, last);
+    return last;
 }
 
 __global__ void __launch_bounds__(THREADS, 2) verify_kernel(VerifyArgs a)
@@ -120,6 +130,7 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(VerifyArgs a)
     __shared__ double part[WARPS];
     __shared__ double cta_sum[2];
     __shared__ int accepted_s;
+    __shared__ Turn turn;
     cg::cluster_group cluster = cg::this_cluster();
     const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int b = blockIdx.x / nc, K = a.max_draft, V = a.vocab;
@@ -176,13 +187,33 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(VerifyArgs a)
                     pv[i] = j < e ? w.p[j] : 0.0f;
                     qv[i] = w.residual && j < e ? w.draft(j) : 0.0f;
                 }
+                // the weights, then their sums; low: what each subtraction and addition rounded off
+                float low[BLOCK];
 #pragma unroll
-                for (int i = 0; i < BLOCK; ++i) pv[i] = w.of(pv[i], qv[i]);
+                for (int i = 0; i < BLOCK; ++i) {
+                    low[i] = 0.0f;
+                    if (w.residual) {
+                        const float d = pv[i] - qv[i];
+                        const bool some = pv[i] > qv[i];
+                        low[i] = some ? (pv[i] - d) - qv[i] : 0.0f;    // exact for p > q >= 0 (Dekker)
+                        pv[i] = some ? d : 0.0f;
+                    } else {
+                        pv[i] = fmaxf(pv[i], 0.0f);                    // a NaN too
+                    }
+                }
 #pragma unroll
                 for (int i = BLOCK / 2; i > 0; i >>= 1)
 #pragma unroll
-                    for (int j = 0; j < i; ++j) pv[j] += pv[j + i];
-                s += pv[0];
+                    for (int j = 0; j < i; ++j) {
+                        const float t = pv[j] + pv[j + i];
+                        low[j] += low[j + i] + lost(pv[j], pv[j + i], t);
+                        pv[j] = t;
+                    }
+                s += (double)pv[0] + (double)low[0];
+            }
+            if (!(s < INFINITY)) {                                     // an infinite weight, or sums past fp32's range
+                s = 0.0;
+                for (int v = v0 + r * run + lane; v < e; v += 32) s += w(v);
             }
             s = warp_sum(s);
             if (lane == r) sums = s;
@@ -226,7 +257,7 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(VerifyArgs a)
                 const unsigned o = __ballot_sync(~0u, start + upto > mark && sums > 0.0), s = __ballot_sync(~0u, sums > 0.0);
                 const int r = o ? __ffs(o) - 1 : 31 - __clz(s);
                 const double c = start + __shfl_sync(~0u, upto - sums, r);
-                const int x = search(w, v0 + r * run, min(v1, v0 + (r + 1) * run), c, mark);
+                const int x = search(w, turn, v0 + r * run, min(v1, v0 + (r + 1) * run), c, mark);
                 if (lane == 0) tokens[n] = x;
             }
         }
@@ -246,9 +277,9 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(VerifyArgs a)
 cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t st)
 {
     // As many CTAs to a request as can all be at work (two on each of 148
-    // SMs), and no more than its row has blocks for.  64 rows of 131072: 17.5
-    // us with 4, 19.8 with 2, 23.5 with 8; 8 of 100003: 10.0 with 8, 12.0 with
-    // 4; 2 of 16384: 8.2 with 2 or more, 9.0 with 1.
+    // SMs), and no more than its row has blocks for.  64 rows of 131072: 17.3
+    // us with 4, 18.3 with 2, 21.9 with 8; 8 of 100003: 8.6 with 8, 11.6 with
+    // 4; 2 of 16384: 6.4 with 2, 6.6 with 4 or 8, 7.8 with 1.
     int nc = MAX_CLUSTER;
     while (nc > 1 && ((int64_t)a.batch * nc > 2 * 148 || a.vocab < nc * WARPS * 32 * BLOCK / 2)) nc /= 2;
     LaunchScope scope(-1, st);

@@ -338,7 +338,8 @@ csa2_status csa2_combine(int32_t n_parts, const float *const *o_parts, const flo
  * max(p_n - q_n, 0) if draft n was refused (from p_n where that is zero
  * everywhere), else from p_n: the first index whose cumulative weight
  * exceeds u[b][max_draft] times the total, weights of zero, negative and NaN
- * being never drawn; 16 weights are added in fp32, those sums in fp64.
+ * being never drawn; the sums are off by at most 2^-42 of themselves and
+ * fp64's rounding.
  *   target [batch][max_draft + 1][vocab] f32: p_i, need not sum to one
  *   probs  [batch][max_draft][vocab] f32: q_i, or NULL for a drafter that
  *          names its token without probabilities (q_i = 1 at that token)
