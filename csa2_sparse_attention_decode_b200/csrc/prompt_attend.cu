@@ -746,7 +746,9 @@ __device__ void softmax(const Args &a, Misc *m, uint8_t *sm)
                     soft_sync();
                     if (tid < RT) {
                         const float top = fmaxf(fmaxf(m->red[0][tid], m->red[1][tid]), fmaxf(m->red[2][tid], m->red[3][tid]));
-                        const float old = m->muse[tid], now = fmaxf(old, top);
+                        // Only a row whose own score is far above its reference moves it: what another row holds, also
+                        // what is not finite, changes no bit of it.
+                        const float old = m->muse[tid], now = top - old > RISE ? top : old;
                         m->fac[r][tid] = ex2(old - now);               // fresh and still fresh: 1; now seen: 0
                         m->muse[tid] = now;
                     }

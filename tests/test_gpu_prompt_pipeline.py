@@ -34,3 +34,23 @@ def test_factors_last_until_the_output_has_used_them(heads, window, f32):
     for t in range(0, n, 250):
         lo = max(0, t + 1 - window) if window else 0
         _check(out[t:t + 250], lse[t:t + 250], _ref(q[t:t + 250], lat[lo:t + 250], t - lo, window), f"tokens from {t}")
+
+
+@pytest.mark.parametrize("value", [float("inf"), -float("inf")])
+@pytest.mark.parametrize("heads,new,past,window,f32", [
+    (64, 700, 0, 128, False), (128, 300, 50, 100, False), (64, 300, 0, 0, False), (128, 100, 500, 0, True),
+    (64, 2, 9000, 0, False), (64, 40, 9000, 0, True), (40, 200, 0, 0, False), (64, 200, 1000, 300, False)])
+def test_infinite_queries_change_no_bit_of_the_others(value, heads, new, past, window, f32):
+    # their scores are +inf or -inf, key by key: one is first without a reference and then far above it
+    q, lat = _inputs(heads + new, [new], [new + past], heads)
+    cu_q, cu_k = _cu([new]), _cu([new + past])
+    clean, clean_lse, _ = _call(q, lat, cu_q, cu_k, window, f32)
+    bad = q.clone()
+    hit = torch.zeros(new, heads, dtype=torch.bool, device="cuda")
+    for t in range(0, new, 3):
+        for h in (t % heads, (7 * t + 1) % heads):
+            bad[t, h, (t * 31 + h) % 512] = value
+            hit[t, h] = True
+    out, lse, err = _call(bad, lat, cu_q, cu_k, window, f32)
+    assert int(err) == 0
+    assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse[~hit], clean_lse[~hit])
