@@ -39,6 +39,7 @@ MAX_SHARDS = 8
 ATTEND_NOALLOC_MAX_ROWS = 512
 MAX_DRAFT, PLAN_MAX_BATCH = 31, 4096
 ROPE_HALVES, ROPE_INVERSE, ROPE_NO_NORM = 1, 2, 4
+PROMPT_WORKSPACE_MAX = 38951424
 KERNEL_BLOCK_SCORE, KERNEL_FLAT_SCORE, KERNEL_POOL_SCORE, KERNEL_SELECT, KERNEL_ATTEND, KERNEL_COMBINE = range(6)
 
 
@@ -442,6 +443,8 @@ def csa2_norm_rope(q, k, pos, inv_freq, q_weight, k_weight, eps: float, q_out, k
 
 
 def csa2_prompt_workspace_bytes(n_q: int, heads: int, n_k: int) -> int:
+    """Workspace of one call of this shape.  Smaller shapes may need more:
+    PROMPT_WORKSPACE_MAX is enough for calls of any shape."""
     return int(lib.csa2_prompt_workspace_bytes(n_q, heads, n_k))
 
 
@@ -450,7 +453,8 @@ def csa2_prompt_attend(q, lat, cu_q, cu_k, window: int, scale: float, out, lse, 
     [n_k, 512] (bf16; rows may lie apart), request b holding tokens
     cu_q[b]..cu_q[b+1] and latents cu_k[b]..cu_k[b+1]; window 0 sees
     everything.  out like q, bf16 or f32; lse [n_q, heads] f32 or None; ws:
-    uint8, csa2_prompt_workspace_bytes(n_q, heads, n_k)."""
+    uint8, csa2_prompt_workspace_bytes(n_q, heads, n_k), or PROMPT_WORKSPACE_MAX
+    where one workspace serves calls of different shapes."""
     n_q, heads = q.shape[:2]
     dev = _device()
     if lat.dtype is not _B16 or lat.dim() != 2 or lat.shape[1] != LATENT or (lat.stride(1) != 1 and lat.numel()):

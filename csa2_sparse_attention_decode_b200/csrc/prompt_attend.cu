@@ -1088,6 +1088,8 @@ constexpr Layout layout()
     return l;
 }
 
+static_assert(layout().bytes == CSA2_PROMPT_WORKSPACE_MAX, "the most that any call needs");
+
 int64_t row_tiles(int64_t n_q, int heads) { return (n_q * heads + RT - 1) / RT; }
 
 // [rows][512] bf16 as 8 slabs of 64 channels, in boxes of box_rows x box_slabs

@@ -429,13 +429,18 @@ csa2_status csa2_norm_rope(int32_t n, int32_t dim, int32_t heads, const uint16_t
  *          weights kept to 16 bits); a query without keys gets zeros
  *   lse [n_q][heads] f32 or NULL: ln sum_j exp(scale * q . lat_j), -inf
  *          without keys; with f32 outputs what csa2_combine takes
- *   ws: at least csa2_prompt_workspace_bytes(), 256-byte aligned; its
- *          contents are not kept.  Calls that may overlap need one each.
+ *   ws: at least csa2_prompt_workspace_bytes() of the call's own n_q, heads
+ *          and n_k, 256-byte aligned; its contents are not kept.  Calls that
+ *          may overlap need one each.  The size does NOT grow with the
+ *          shape: few queries over many latents need 39 MB, many queries 256
+ *          bytes.  A workspace for calls of different shapes is sized by
+ *          CSA2_PROMPT_WORKSPACE_MAX, which is enough for any.
  * Tokens from cu_q[batch] on are left as they were.  A latent that is not
  * finite leaves the queries that see it no finite output in its channel (a
  * NaN: in none) and changes no other query's, nor does a query that is not
  * finite.  cu_q or cu_k that fall or pass n_q or n_k set CSA2_DEV_BAD_REQUEST; nothing outside the
  * given arrays is read or written.  heads 1..128, n_q * heads < 2^31 - 64. */
+#define CSA2_PROMPT_WORKSPACE_MAX ((size_t)38951424)
 size_t csa2_prompt_workspace_bytes(int32_t n_q, int32_t heads, int32_t n_k);
 csa2_status csa2_prompt_attend(int32_t batch, const int32_t *cu_q, const int32_t *cu_k, int32_t n_q, int32_t n_k,
                                int32_t heads, const uint16_t *q, const uint16_t *lat, int64_t lat_stride,
