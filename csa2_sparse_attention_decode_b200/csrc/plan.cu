@@ -117,7 +117,8 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(PlanArgs a)
     }
     if (n_free != n_free_in && first && threadIdx.x == 0) set_error(a.error, CSA2_DEV_BAD_REQUEST);
     const Pair start = block_exclusive({s_rel, s_tok}, red, total);
-    int64_t top = n_free + total.a;
+    const int64_t released = total.a;
+    int64_t top = n_free + released;
     if (top > a.n_pages) {                                             // more pages than exist: a corrupt table
         if (first && threadIdx.x == 0) set_error(a.error, CSA2_DEV_CAPACITY);
         top = a.n_pages;
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(PlanArgs a)
     if (threadIdx.x == 0) {
         cu[B] = (int)n_tok;
         taken[B] = (int)n_get;
-        rel[B] = (int)(top - n_free);                                  // what fits on the stack
+        rel[B] = (int)min(released, (int64_t)INT32_MAX);
     }
     __syncthreads();
 
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(PlanArgs a)
     // Pages from the last thread down, tokens from the first up: in a small
     // step their loads do not wait for one another.
     const int gt = blockIdx.x * THREADS + threadIdx.x, threads = gridDim.x * THREADS, down = threads - 1 - gt;
-    for (int k = down; k < rel[B]; k += threads) {                     // released pages onto the stack
+    for (int k = down; k < (int)top - n_free; k += threads) {          // released pages onto the stack, as many as it has room for
         const int r = segment_of(rel, B, k);
         const int need = owned[r] - (rel[r + 1] - rel[r]);
         a.free_pages[n_free + k] = a.page_table[(size_t)r * a.max_pages + need + (k - rel[r])];

@@ -366,6 +366,8 @@ csa2_status csa2_verify(int32_t batch, int32_t max_draft, int32_t vocab, const f
  * in order: one whose tokens do not fit max_new, or whose pages the stack no
  * longer holds, gets neither, like every later one that needs some
  * (CSA2_DEV_CAPACITY); bad lengths or m get nothing (CSA2_DEV_BAD_REQUEST).
+ * Released pages that would pass n_pages on the stack (some are in it twice)
+ * are left out, the last ones (CSA2_DEV_CAPACITY).
  * n_tokens is not changed: csa2_prefill and csa2_append count tokens in.
  *   page_table [batch][max_pages], free_pages [n_pages]: updated in place
  *   n_free, n_free_out: one word each, before and after; not the same word
