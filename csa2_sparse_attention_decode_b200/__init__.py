@@ -387,7 +387,8 @@ def csa2_plan_tokens(n_tokens, n_new, m, page_table, free_pages, n_free, n_free_
     """Pages and slots of a step's new tokens (int32 tensors throughout):
     n_tokens, n_new, m [batch]; page_table [batch, max_pages] and free_pages
     [n_pages] are updated; n_free, n_free_out [1]; cu_new [batch+1];
-    token_req, token_pos, token_slot [max_new]."""
+    token_req, token_pos, token_slot [max_new].  Dropped tokens that were in
+    the cache: csa2_prefill writes the window of those that stay again."""
     B, width = page_table.shape
     one, per, rows, dev = (1,), (B,), token_req.shape, _device()
     n_pages = free_pages.shape[0]

@@ -156,7 +156,8 @@ size_t csa2_workspace_bytes(int32_t batch, int32_t max_entries);
  * n_tokens[req] = tok_begin + n_tok.
  *   lat  [n_tok][512] f32, key [n_tok][128] f32, gate [n_tok] f32 (device).
  *   tok_begin must be a multiple of m (read from m_host, which must equal
- *   cache->m[req]); calls for one request go in increasing tok_begin. */
+ *   cache->m[req]); calls for one request go in increasing tok_begin, but
+ *   for the window that is written again after a drop (csa2_plan_tokens). */
 csa2_status csa2_prefill(const csa2_cache *cache, int32_t req, int32_t m_host,
                          int32_t tok_begin, int32_t n_tok, int32_t n_tok_final,
                          const float *lat, const float *key, const float *gate,
@@ -357,7 +358,7 @@ csa2_status csa2_verify(int32_t batch, int32_t max_draft, int32_t vocab, const f
 
 /* Pages and slots for a step's tokens.  Request b holds n_tokens[b] tokens
  * (compression m[b], 1 or 2) and gains n_new[b] of them, or drops -n_new[b]
- * (rejected drafts; all of them when it ends).  It owns the first
+ * (all of them when it ends).  It owns the first
  * ceil((n_tokens / m) / 64) entries of its page_table row.  Pages it no
  * longer needs are pushed on the stack free_pages[0 .. *n_free), in request
  * order and ascending within a request; then the pages it comes to need are
@@ -369,6 +370,14 @@ csa2_status csa2_verify(int32_t batch, int32_t max_draft, int32_t vocab, const f
  * Released pages that would pass n_pages on the stack (some are in it twice)
  * are left out, the last ones (CSA2_DEV_CAPACITY).
  * n_tokens is not changed: csa2_prefill and csa2_append count tokens in.
+ * A drop is of pages alone.  Tokens that csa2_append or csa2_prefill has
+ * written, and of which some are dropped again, have overwritten older tokens
+ * of the window's ring, the pending token of an m = 2 pair and the summary of
+ * the last block.  Before anything else reads or extends such a request of
+ * n remaining tokens, csa2_prefill writes its window again: tokens
+ * [t, n) with t = max(0, n - 128) rounded down to a multiple of m and
+ * n_tok_final = n, which also sets n_tokens.  (Drafts that csa2_verify
+ * refuses before they are written need none of this.)
  *   page_table [batch][max_pages], free_pages [n_pages]: updated in place
  *   n_free, n_free_out: one word each, before and after; not the same word
  *   cu_new [batch + 1]: prefix sum of the granted tokens
