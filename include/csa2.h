@@ -431,13 +431,23 @@ csa2_status csa2_norm_rope(int32_t n, int32_t dim, int32_t heads, const uint16_t
  * `window` of them:
  *   o = sum_j softmax_j(scale * q . lat_j) lat_j
  * It is what a layer that sees its window alone computes for a prompt
- * (window = CSA2_SWA), and a whole layer while every entry is selected
- * (window = 0); with n = 1 it is a decode step over raw latents.
+ * (window = CSA2_SWA), before its latents are rounded to the cache's FP8.
+ * With window = 0 it is dense attention over raw latents, and with n = 1 a
+ * decode step of it: NOT csa2_attend with every entry selected, which counts
+ * the window's tokens twice (as entries and as the window), sees m = 2 pairs
+ * as one latent, and reads FP4 entries.  The prompt's counterpart of that
+ * decode, for m = 1 while every entry is selected, is two calls, window =
+ * CSA2_SWA and window = 0, f32 both, joined by csa2_combine.
  *   cu_q, cu_k [batch + 1] i32, from 0, non-decreasing; q [n_q][heads][512]
  *          bf16; lat [n_k] rows of 512 bf16, lat_stride elements apart (a
  *          multiple of 8)
- *   out [n_q][heads][512] bf16, or f32 (out_is_fp32 = 1, with the softmax
- *          weights kept to 16 bits); a query without keys gets zeros
+ *   out [n_q][heads][512] bf16, or f32 (out_is_fp32 = 1); a query without
+ *          keys gets zeros.  The softmax weights are fp32 in their sum; where
+ *          they multiply latents, bf16 outputs have them rounded to bf16 (off
+ *          by at most 2^-8 of themselves, which adds up to a third to the
+ *          output's own rounding) and f32 outputs keep twice those bits.
+ *          csa2_attend keeps the latter for either type: ask for f32 where a
+ *          bf16 result has to be that exact
  *   lse [n_q][heads] f32 or NULL: ln sum_j exp(scale * q . lat_j), -inf
  *          without keys; with f32 outputs what csa2_combine takes
  *   ws: at least csa2_prompt_workspace_bytes() of the call's own n_q, heads
@@ -449,8 +459,9 @@ csa2_status csa2_norm_rope(int32_t n, int32_t dim, int32_t heads, const uint16_t
  * Tokens from cu_q[batch] on are left as they were.  A latent that is not
  * finite leaves the queries that see it no finite output in its channel (a
  * NaN: in none) and changes no other query's, nor does a query that is not
- * finite.  cu_q or cu_k that fall or pass n_q or n_k set CSA2_DEV_BAD_REQUEST; nothing outside the
- * given arrays is read or written.  heads 1..128, n_q * heads < 2^31 - 64. */
+ * finite.  cu_q or cu_k that fall or pass n_q or n_k set
+ * CSA2_DEV_BAD_REQUEST; nothing outside the given arrays is read or written.
+ * heads 1..128, n_q * heads < 2^31 - 64. */
 #define CSA2_PROMPT_WORKSPACE_MAX ((size_t)38951424)
 size_t csa2_prompt_workspace_bytes(int32_t n_q, int32_t heads, int32_t n_k);
 csa2_status csa2_prompt_attend(int32_t batch, const int32_t *cu_q, const int32_t *cu_k, int32_t n_q, int32_t n_k,
