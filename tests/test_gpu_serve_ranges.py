@@ -1,0 +1,88 @@
+"""The calls around the layers at the far ends of what they take: vocabularies up to 2^28, 1024 heads, and prompt
+attention over more row tiles than several SMs may share."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+def _csa2():
+    import csa2_sparse_attention_decode_b200 as csa2
+    return csa2
+
+
+@pytest.mark.parametrize("V", [2200003, 5000000])
+@pytest.mark.parametrize("kind", ["usual", "peaked"])
+def test_verify_rows_of_millions(V, kind):
+    # several blocks of weights a lane, and a search of several rounds
+    from test_gpu_verify_sums import _draw, _row
+    r = np.random.default_rng(V)
+    target = np.repeat(_row(r, V, kind)[None, None], 2, 1)
+    draft = int(r.integers(0, V))
+    target[0, 0, draft] = 0
+    probs = _row(r, V, "flat")[None, None]
+    u = r.random(6).astype(np.float32)
+    for q in (None, probs):
+        w = target[0, 0].astype(np.longdouble)
+        w = w if q is None else np.maximum(w - q[0, 0].astype(np.longdouble), 0)
+        c = np.cumsum(w)
+        mark = u.astype(np.longdouble) * c[-1]
+        at = np.searchsorted(c, mark, side="right")
+        gap = np.minimum(c[at] - mark, mark - c[np.maximum(at - 1, 0)]) / c[-1]
+        fine = gap > 4 * V * 2.0 ** -53        # as in the test of marks next to a border
+        assert fine.sum() >= 3
+        got = _draw(target, q, draft, np.stack([np.full(6, 0.5, np.float32), u], 1))
+        assert got[fine].tolist() == at[fine].tolist()
+
+
+@pytest.mark.slow
+def test_verify_the_largest_vocabulary():
+    csa2 = _csa2()
+    V, B, step = 1 << 28, 5, 1024
+    target = torch.zeros(B, 1, V, device="cuda")
+    target[:, :, 7::step] = 1                  # 2^18 weights: every mark below lies in the middle of one
+    k = [0, 1, 77777, (1 << 18) - 2, (1 << 18) - 1]
+    u = torch.tensor([[(x + 0.5) / (1 << 18)] for x in k], device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    acc, tok, err = torch.full((B,), -9, **i32), torch.full((B, 1), -9, **i32), torch.zeros(1, **i32)
+    csa2.csa2_verify(target, None, torch.zeros(B, 0, **i32), torch.zeros(B, **i32), u, acc, tok, err)
+    assert int(err) == 0 and acc.tolist() == [0] * B and tok[:, 0].tolist() == [7 + step * x for x in k]
+
+
+@pytest.mark.parametrize("dim", [64, 512])
+@pytest.mark.parametrize("heads,kv", [(1024, 1024), (1023, 0), (0, 1021), (1, 1024)])
+@pytest.mark.parametrize("halves", [False, True])
+def test_norm_of_a_thousand_heads(dim, heads, kv, halves):
+    from test_gpu_serve import _check_norm, _freq, _norm_ref
+    csa2 = _csa2()
+    g = torch.Generator(device="cuda").manual_seed(heads + kv + dim)
+    n = 5
+    x = torch.randn(n, heads + kv, dim, generator=g, device="cuda").to(torch.bfloat16)
+    q, k = (x[:, :heads] if heads else None), (x[:, heads:] if kv else None)
+    pos = torch.randint(0, 1 << 20, (n,), generator=g, device="cuda", dtype=torch.int32)
+    w, freq = torch.randn(dim, generator=g, device="cuda"), _freq(32)
+    qo = torch.empty(n, heads, dim, dtype=torch.bfloat16, device="cuda") if heads else None
+    ko, kf = (torch.empty(n, kv, dim, dtype=t, device="cuda") if kv else None for t in (torch.bfloat16, torch.float32))
+    csa2.csa2_norm_rope(q, k, pos, freq, w if heads else None, w if kv else None, 1e-6, qo, ko, kf,
+                        flags=csa2.ROPE_HALVES if halves else 0)
+    for got, src in ((qo, q), (ko, k), (kf, k)):
+        if got is not None:
+            _check_norm(got, *_norm_ref(src, w, pos, freq, halves, 1e-6), "heads")
+
+
+@pytest.mark.parametrize("f32", [False, True])
+def test_whole_row_tiles_whose_tokens_straddle_them(f32):
+    # 20 heads: 64-row tiles begin and end inside tokens; over 896 tiles, no window, several requests
+    from test_gpu_prompt import _check_all
+    _check_all([1500, 1, 0, 1399], [0, 700, 3, 200], 20, 0, f32, seed=20, extra_q=7)
+
+
+@pytest.mark.parametrize("heads", [64, 65])
+def test_decode_tokens_past_the_shared_row_tiles(heads):
+    # more single tokens than the split path plans, with pasts from nothing to many key tiles
+    from test_gpu_prompt import _check_all
+    n = 1000
+    past = [(i * 37) % 300 for i in range(n)]
+    past[n // 3], past[-1] = 5000, 3000
+    _check_all([1] * n, past, heads, 0, False, seed=heads)
