@@ -22,7 +22,15 @@
 //
 // P is rounded to bf16 for the second product (off by at most 2^-8 of itself,
 // as the bf16 output is); for an fp32 output it is split into two bf16 parts
-// (2^-16) and the product taken twice.
+// (2^-16) and the product taken twice.  Doing that for bf16 outputs too would
+// take their error from 0.0022 to 0.0017 (windows of 128; 0.0019 to 0.0017
+// for 6000 causal tokens) and cost 42 % there, 18 % for ragged decode tokens.
+//
+// The tensor cores round every sum toward zero: O loses 2^-22 of itself, on
+// average, with each key tile, 2^-12 over 131072 latents.  An fp32 output is
+// therefore collected in memory, with ordinary additions, every 16 key tiles.
+// A bf16 output is not: the loss reaches half a step of it, 2^-8, where one
+// CTA takes a row over some 2 million latents.
 //
 // Roles: eight warps do the softmax and the output, one warp plans the row
 // tiles and issues the TMA loads, one issues the MMAs.  A 128-dim chunk of
@@ -74,6 +82,10 @@ constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float RISE = 32.0f;                  // how far (in log2) a score may pass the reference
 constexpr float FRESH = -3.0e38f;              // reference of a row that has seen no key: every score passes it
 constexpr int CTAS = 148;                      // one per SM
+// Key tiles whose products one O takes for an fp32 output.  1000 tokens over
+// 131072 latents are off by 4.6e-6 (7.4e-6 over latents of one sign, which
+// pass 1e-5 with 24), uncut by 2.5e-4; 6000 causal tokens take 4.2 ms, 3.7.
+constexpr int CUT = 16;
 // A share of the units ends at a row tile's border if one is this near: a part
 // costs its way through memory and the join (8 ragged tokens 30 us with 2,
 // 24 with 0 or 1; 400 tokens after 1000 latents 98 with 1, 101 with 0 or 2).
@@ -87,13 +99,18 @@ enum Deal {
     SLIDING                                    // runs of single-token row tiles whose keys fit one key tile
 };
 
+// Whether a run of key tiles is cut: a sliding window's is one.
+template <bool SPLIT_P, Deal DEAL>
+constexpr bool CUTS = SPLIT_P && DEAL != SLIDING;
+
 struct Segment {                               // n consecutive key tiles of one row tile
     int tile, n, key0;                         // key0: first key of the first of them; key key0 + i lies in row
                                                // (i + turn) % 128 of the tile
     int max_lo, min_hi;                        // keys in [max_lo, min_hi) are seen by every live row
     int slot;                                  // partial result's slot, -1: the segment is the whole row tile
-    bool uniform;                              // every row sees [max_lo, min_hi), which is not empty
-    bool boxed;                                // every row that exists belongs to a request
+    bool uniform : 1;                          // every row sees [max_lo, min_hi), which is not empty
+    bool boxed : 1;                            // every row that exists belongs to a request
+    bool again : 1, more : 1;                  // an earlier, a later segment has other key tiles of the same run
     uint8_t turn;
 };
 
@@ -311,7 +328,7 @@ __device__ __forceinline__ float columns(float (&v)[32])
 // SLIDING: a token's keys are the last token's, one in and one out.  The tile
 // is a ring then: key k lies in row (k - base) % 128, the new latent goes
 // over the one that left, and 1 KB comes in a token instead of 128 KB.
-template <Deal DEAL>
+template <bool SPLIT_P, Deal DEAL>
 __device__ void producer(const Args &a, Misc *m, uint8_t *sm, const CUtensorMap *map_q, const CUtensorMap *map_k)
 {
     const int lane = threadIdx.x & 31;
@@ -326,18 +343,28 @@ __device__ void producer(const Args &a, Misc *m, uint8_t *sm, const CUtensorMap 
         last = (int)(tiles * (blockIdx.x + 1) / gridDim.x);
     }
     int left = DEAL == SHARED ? share.units : 0;
+    int runs = 0, rest = 0, resume = 0;                                // CUTS: key tiles of the run behind this segment, its next key
+    constexpr Segment NOTHING = {-1, 0, 0, 0, 0, -1, false, false, false, false, 0};
+    Segment g = NOTHING;
+    uint32_t queries = 0;                                              // loads of them
     Request req = {-1, 0, 0};
     int base = 0, top = -1;                                            // SLIDING: the ring holds keys [top - 128, top)
     uint32_t unit = 0;
     for (uint32_t s = 0;; ++s) {
-        Segment g = {-1, 0, 0, 0, 0, -1, false, false, 0};
-        if (DEAL == SHARED) {
+        const bool again = CUTS<SPLIT_P, DEAL> && rest > 0;
+        if (!again) g = NOTHING;
+        g.again = again;
+        if (again) {                                                   // the run goes on
+            g.key0 = resume;
+            g.n = rest;
+        } else if (DEAL == SHARED) {
             for (; left > 0 && tile < last; ++tile, at = 0) {
                 const int total = key_tiles(a, live, tile, at, g.key0);
                 if (total - at <= 0) continue;
                 g.tile = tile;
                 g.n = min(left, total - at);
-                if (g.n < total) g.slot = 2 * blockIdx.x + (s == 0 ? 0 : 1);
+                if (g.n < total) g.slot = 2 * blockIdx.x + (runs == 0 ? 0 : 1);
+                ++runs;
                 left -= g.n;
                 ++tile;
                 at = 0;
@@ -355,6 +382,11 @@ __device__ void producer(const Args &a, Misc *m, uint8_t *sm, const CUtensorMap 
         } else if (tile < last) {
             g.tile = tile++;
             g.n = 1;
+        }
+        if (CUTS<SPLIT_P, DEAL>) {
+            rest = max(0, g.n - CUT);
+            g.more = rest > 0;
+            g.n -= rest;
         }
         int lo[2] = {0, 0}, hi[2] = {-1, -1};                          // hi < 0: no such row
         if (DEAL == SLIDING && g.tile >= 0) {                          // rows of one token
@@ -419,15 +451,16 @@ __device__ void producer(const Args &a, Misc *m, uint8_t *sm, const CUtensorMap 
         if (ok && lane == 0) mbar_arrive(&m->seg_full[r]);
         if (ok && g.tile < 0) return;
 
-        ok = ok && warp_wait(m, &m->q_empty, (s & 1) ^ 1);
-        if (ok && elect_one()) {
+        if (!again) ok = ok && warp_wait(m, &m->q_empty, (queries++ & 1) ^ 1);
+        if (ok && !again && elect_one()) {
             mbar_arrive_expect_tx(&m->q_full, 8 * Q_SLAB);
             tma_load_3d(sm + Q_OFF, map_q, 0, g.tile * RT, 0, &m->q_full);
             // the rows after these come to L2 meanwhile: from memory they would arrive after the last product
             if (DEAL == SLIDING) tma_prefetch_3d(map_q, 0, (g.tile + 1) * RT, 0);
         }
         int key0 = DEAL == SLIDING ? base : g.key0;
-        for (int k = 0; ok && k < g.n; ++k, ++unit, key0 = next_tile(g, m->lo[r], m->hi[r], key0)) {
+        for (int k = 0; ok && k < g.n; ++k, ++unit) {
+            const int next = next_tile(g, m->lo[r], m->hi[r], key0);   // before its last load: then lo may be written
 #pragma unroll 1
             for (int c = 0; c < CHUNKS; ++c) {
                 ok = warp_wait(m, &m->k_empty[c], (unit & 1) ^ 1);
@@ -451,7 +484,9 @@ __device__ void producer(const Args &a, Misc *m, uint8_t *sm, const CUtensorMap 
                     tma_load_3d(sm + K_OFF + 2 * c * K_SLAB, map_k, 0, key0, 2 * c, &m->k_full[c]);
                 }
             }
+            key0 = next;
         }
+        resume = key0;
         if (!ok) {                                                     // gave up: no copy may be in flight at exit
             for (int parity = 0; parity < 2; ++parity) {
                 mbar_wait(&m->q_full, parity, 1u << 16);
@@ -463,7 +498,7 @@ __device__ void producer(const Args &a, Misc *m, uint8_t *sm, const CUtensorMap 
 }
 
 // Issues every product.
-template <bool SPLIT_P>
+template <bool SPLIT_P, Deal DEAL>
 __device__ void mma_issuer(Misc *m, uint8_t *sm)
 {
     // Descriptors of the operands' first steps; a step on adds its bytes / 16.
@@ -473,15 +508,19 @@ __device__ void mma_issuer(Misc *m, uint8_t *sm)
     uint32_t unit = 0;
     // The next segment is looked up before the last product of this one, so
     // that nothing stands between that product and the next S.
+    bool again = false, more = false;                                  // of the segment looked up last
     auto length = [&](uint32_t s) {
         if (!wait(m, &m->seg_full[s & 1], (s >> 1) & 1)) return 0;
         const int n = m->seg[s & 1].n;
+        again = CUTS<SPLIT_P, DEAL> && m->seg[s & 1].again;
+        more = CUTS<SPLIT_P, DEAL> && m->seg[s & 1].more;
         mbar_arrive(&m->seg_empty[s & 1]);
         return n;
     };
     int n = length(0);
+    uint32_t queries = 0;
     for (uint32_t s = 0; n > 0; ++s) {
-        if (!wait(m, &m->q_full, s & 1)) return;
+        if (!again && !wait(m, &m->q_full, queries++ & 1)) return;
         int next = 0;
         for (int k = 0; k < n; ++k, ++unit) {
 #pragma unroll
@@ -494,7 +533,7 @@ __device__ void mma_issuer(Misc *m, uint8_t *sm)
             }
             mma_commit(&m->s_full);
             if (k == n - 1) {
-                mma_commit(&m->q_empty);
+                if (!more) mma_commit(&m->q_empty);
                 next = length(s + 1);
             }
             if (k == 0 && !wait(m, &m->o_empty, (s & 1) ^ 1)) return;  // the last row tile's output is out of O
@@ -554,8 +593,9 @@ __device__ __forceinline__ void o_read(Misc *m)
 // which two warps fill and a bulk store takes away.  (Element stores of the same lines, shuffled or staged, took 5500
 // cycles a row tile: the next S leaves the shared-memory pipe little time.)
 // f32: a warp's 32 channels are a line, stored as they are.
-// A part keeps f32 sums, four rows side by side.
-template <bool SPLIT_P>
+// A part keeps f32 sums, four rows side by side.  Further segments of a run are
+// added to what its first one left there, the same thread's words.
+template <bool SPLIT_P, Deal DEAL>
 __device__ void store(const Args &a, Misc *m, uint8_t *stage, const CUtensorMap *map_out)
 {
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3, mate = w & 1, group = w >> 1;
@@ -565,10 +605,15 @@ __device__ void store(const Args &a, Misc *m, uint8_t *stage, const CUtensorMap 
     for (uint32_t s = 0;; ++s) {
         const uint32_t r = s & 1;
         if (group_any(group, !wait(m, &m->seg_full[r], (s >> 1) & 1))) break;          // both warps leave, or none
-        const int tile = m->seg[r].tile, slot = m->seg[r].slot;
+        const int tile = m->seg[r].tile, slot = DEAL == SHARED ? m->seg[r].slot : -1;
         const bool boxed = m->seg[r].boxed;
         const uint32_t live[2] = {__ballot_sync(~0u, m->hi[r][lane] >= 0), __ballot_sync(~0u, m->hi[r][32 + lane] >= 0)};
-        if (lane == 0) mbar_arrive(&m->seg_empty[r]);
+        const bool again = CUTS<SPLIT_P, DEAL> && m->seg[r].again, more = CUTS<SPLIT_P, DEAL> && m->seg[r].more;
+        const float *old_fac = reinterpret_cast<const float *>(m->lo[r]);      // softmax leaves them there
+        if (!again) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&m->seg_empty[r]);
+        }
         if (tile < 0) break;
         wait(m, &m->fac_full[r], (s >> 1) & 1);
         wait(m, &m->o_full, s & 1);
@@ -580,24 +625,40 @@ __device__ void store(const Args &a, Misc *m, uint8_t *stage, const CUtensorMap 
             for (int ch = 0; ch < 2 * CHUNKS; ++ch) {
                 const int c = ch >> 1, half = ch & 1, d = 128 * c + 32 * w + lane;
                 uint32_t o[32];
+                float *part = a.part_o + (size_t)max(slot, 0) * RT * D;
+                float *out = (float *)a.out + (size_t)(row0 + 32 * half) * D + d;
+                float old[32];
+                if (again) {
+                    if (slot >= 0) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            *reinterpret_cast<float4 *>(old + j) = *reinterpret_cast<const float4 *>(part + part_at(32 * half + j, d));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) old[j] = live[half] >> j & 1 ? out[(size_t)j * D] : 0.0f;
+                    }
+                }
                 tmem_ld32(tb + RT * c + 32 * half, o);
                 tmem_ld_wait();
-                if (slot < 0)
+                if (again)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(fmaf(old[j], old_fac[32 * half + j], __uint_as_float(o[j])));
+                if (slot < 0 && !more)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fac[32 * half + j]);
                 if (ch == 2 * CHUNKS - 1) o_read(m);
                 if (slot >= 0) {
-                    float *part = a.part_o + (size_t)slot * RT * D;
 #pragma unroll
                     for (int j = 0; j < 32; j += 4)
                         *reinterpret_cast<uint4 *>(part + part_at(32 * half + j, d)) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
                 } else {
-                    float *out = (float *)a.out + (size_t)(row0 + 32 * half) * D + d;
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         if (live[half] >> j & 1) out[(size_t)j * D] = __uint_as_float(o[j]);
                 }
             }
+            __syncwarp();
+            if (again && lane == 0) mbar_arrive(&m->seg_empty[r]);
         } else {
             float2 f[8];                                               // of rows 8i + 2 (lane % 4) and the next
 #pragma unroll
@@ -655,16 +716,18 @@ __device__ void softmax(const Args &a, Misc *m, uint8_t *sm)
     uint8_t *bad_key = P;                                              // [2][KT], while P is not in use
     const float4 *muse4 = reinterpret_cast<const float4 *>(m->muse + 32 * half);
     uint32_t unit = 0;
+    float kept = 0.0f, kept_at = 0.0f;                                 // CUTS: row tid's sum over the run's segments so far, its reference
     for (uint32_t s = 0;; ++s) {
         const uint32_t r = s & 1;
         if (soft_any(!wait(m, &m->seg_full[r], (s >> 1) & 1))) break;  // all eight warps leave, or none; muse and P are free
         const Segment g = m->seg[r];
         if (g.tile < 0) break;
         const int *lo = m->lo[r] + 32 * half, *hi = m->hi[r] + 32 * half;
+        const bool again = CUTS<SPLIT_P, DEAL> && g.again, more = CUTS<SPLIT_P, DEAL> && g.more;
         float l[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) l[j] = 0.0f;
-        if (!g.uniform && tid < RT) m->muse[tid] = FRESH;
+        if (!g.uniform && !again && tid < RT) m->muse[tid] = FRESH;
 
         int key0 = g.key0;
         for (int k = 0; k < g.n; ++k, ++unit, key0 = next_tile(g, m->lo[r], m->hi[r], key0)) {
@@ -673,7 +736,7 @@ __device__ void softmax(const Args &a, Misc *m, uint8_t *sm)
             wait(m, &m->s_full, unit & 1);                             // given up: finish the segment, then leave
             fence_after_sync();
             float x[32];
-            bool exact = k == 0 && !g.uniform;                         // find the rows' maxima first
+            bool exact = k == 0 && !again && !g.uniform;               // find the rows' maxima first
             for (;;) {
                 {
                     uint32_t raw[32];
@@ -768,7 +831,7 @@ __device__ void softmax(const Args &a, Misc *m, uint8_t *sm)
                         }
                         tmem_st_wait();
                     }
-                } else if (k == 0) {
+                } else if (k == 0 && !again) {
                     // A row's first reference: any score near the maximum will
                     // do, so where all rows see the same keys the first of
                     // them gives it.
@@ -815,11 +878,20 @@ __device__ void softmax(const Args &a, Misc *m, uint8_t *sm)
         soft_sync();
         const int64_t row0 = (int64_t)g.tile * RT;
         if (tid < RT) {
-            const float sum = (m->red[0][tid] + m->red[1][tid]) + (m->red[2][tid] + m->red[3][tid]);
+            float sum = (m->red[0][tid] + m->red[1][tid]) + (m->red[2][tid] + m->red[3][tid]);
+            if (CUTS<SPLIT_P, DEAL>) {
+                if (again) {
+                    const float old = ex2(kept_at - m->muse[tid]);
+                    sum += old * kept;
+                    m->lo[r][tid] = __float_as_int(old);               // nobody reads the rows' ranges any more
+                }
+                kept = sum;
+                kept_at = m->muse[tid];
+            }
             const bool none = m->muse[tid] == FRESH && !(sum != sum);  // no key seen (a NaN sum has seen one)
-            if (g.slot >= 0) {
+            if (!more && g.slot >= 0) {
                 a.part_ml[(size_t)g.slot * RT + tid] = make_float2(none ? -INFINITY : m->muse[tid], none ? 0.0f : sum);
-            } else {
+            } else if (!more) {
                 m->fac[r][tid] = none ? 0.0f : 1.0f / sum;
                 if (a.lse && m->hi[r][tid] >= 0)
                     a.lse[row0 + tid] = none ? -INFINITY : (m->muse[tid] + log2f(sum)) * LN2;
@@ -956,13 +1028,13 @@ prompt_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     if (warp < SOFT_WARPS) {
         softmax<SPLIT_P, DEAL>(a, m, sm);
     } else if (warp < LOAD_WARP) {
-        store<SPLIT_P>(a, m, sm + P_OFF + P_BYTES, &map_out);
+        store<SPLIT_P, DEAL>(a, m, sm + P_OFF + P_BYTES, &map_out);
     } else if (warp == LOAD_WARP) {
         if (DEAL == SHARED) fence_proxy_async_smem();                  // the plan's scratch lies where the latents land
-        producer<DEAL>(a, m, sm, &map_q, &map_k);
+        producer<SPLIT_P, DEAL>(a, m, sm, &map_q, &map_k);
     } else {
         if (elect_one()) {
-            mma_issuer<SPLIT_P>(m, sm);
+            mma_issuer<SPLIT_P, DEAL>(m, sm);
             mma_commit(&m->drain);                                     // no MMA may be in flight at exit
             mbar_wait(&m->drain, 0);
         }

@@ -447,7 +447,9 @@ csa2_status csa2_norm_rope(int32_t n, int32_t dim, int32_t heads, const uint16_t
  *          by at most 2^-8 of themselves, which adds up to a third to the
  *          output's own rounding) and f32 outputs keep twice those bits.
  *          csa2_attend keeps the latter for either type: ask for f32 where a
- *          bf16 result has to be that exact
+ *          bf16 result has to be that exact.  bf16 outputs of many queries
+ *          also lose 2^-22 of themselves for each 128 latents they see; f32
+ *          outputs do not
  *   lse [n_q][heads] f32 or NULL: ln sum_j exp(scale * q . lat_j), -inf
  *          without keys; with f32 outputs what csa2_combine takes
  *   ws: at least csa2_prompt_workspace_bytes() of the call's own n_q, heads

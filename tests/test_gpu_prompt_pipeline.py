@@ -54,3 +54,32 @@ def test_infinite_queries_change_no_bit_of_the_others(value, heads, new, past, w
     out, lse, err = _call(bad, lat, cu_q, cu_k, window, f32)
     assert int(err) == 0
     assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse[~hit], clean_lse[~hit])
+
+
+@pytest.mark.parametrize("heads,new,past,window", [
+    (64, [1000], [60000], 0), (64, [300], [60000], 0), (20, [3, 2900], [40000, 50000], 0), (64, [200], [70000], 65000),
+    (128, [500, 1, 30], [1900, 50000, 40000], 0), (33, [800, 700], [2500, 9000], 5000), (64, [6000], [0], 0)])
+def test_f32_outputs_over_many_latents(heads, new, past, window):
+    # Latents of one sign, so that what the sums lose shows.  A score is off by err and a weight, in two bf16 parts,
+    # by 2^-16; 16 key tiles of 16 products are added toward zero, each off by at most 2^-23 of a sum that grows
+    # from nothing, half that of it all: 2^-16; fp32 additions of those sums over the past (500 at most) 2^-15 for the worst,
+    # but their errors have either sign: 2^-19.
+    kv = [n + p for n, p in zip(new, past)]
+    q, lat = _inputs(heads, new, kv, heads)
+    lat = lat.abs()
+    q *= 0.5
+    out, lse, err = _call(q, lat, _cu(new), _cu(kv), window, True)
+    assert int(err) == 0
+    a = c = 0
+    for n, k in zip(new, kv):
+        for t in sorted({0, n // 3, n - 1}):
+            hi = k - n + t + 1
+            lo = max(0, hi - window) if window else 0
+            o, l, mag, e = _ref(q[a + t:a + t + 1], lat[c + lo:c + hi], hi - lo - 1, 0)
+            got = out[a + t:a + t + 1].double()
+            tol = (2 * 2.0 ** -16 + 2.0 ** -19 + 2 * e) * mag
+            assert ((got - o).abs() <= tol).all(), float(((got - o).abs() / mag).max())
+            # and in the mean, without the worst of every rounding
+            assert float((got - o).norm() / o.norm()) < 1e-5
+            assert ((lse[a + t:a + t + 1].double() - l).abs() <= e[..., 0] + 2.0 ** -20 * (1 + l.abs())).all()
+        a, c = a + n, c + k
