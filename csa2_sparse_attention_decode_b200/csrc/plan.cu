@@ -8,8 +8,8 @@
 // batch (released pages, taken pages, granted tokens) place everything.
 //
 // Bound: 12 bytes written per new token (request, position, slot); a decode
-// step's 64 tokens are pure latency (4.8 us, of them 2.5 the launch).  So one launch does it all, and no CTA
-// waits for another: each repeats the prefix sums (two loads' latency and
+// step's 64 tokens are pure latency (4.8 us, of them 2.5 the launch).  So one
+// launch does it all, and no CTA waits for another: each repeats the prefix sums (two loads' latency and
 // three block scans) and then takes its share of the tokens.  That works
 // because nothing a CTA reads is written in the same launch: a taken page is
 // looked up in the old stack, or, above n_free, in the tables of the requests
@@ -261,9 +261,9 @@ cudaError_t launch_plan(const PlanArgs &a, cudaStream_t st)
         });
     if (e != cudaSuccess) return e;
     // 1024 tokens a CTA; and, since releases can be many pages whatever the
-    // tokens (300 requests, a quarter of them dropping tokens: 8.2 us with two
-    // CTAs, 7.1 with 8 or more), 16 requests a CTA.  More than two CTAs an SM
-    // only repeat the prefix sums (295000 tokens: 5.4 us with 296, 7.3 with
+    // tokens (300 requests, a quarter of them dropping tokens: 8.3 us with two
+    // CTAs, 7.2 with 8 or more), 16 requests a CTA.  More than two CTAs an SM
+    // only repeat the prefix sums (295000 tokens: 5.6 us with 296, 7.4 with
     // 592, 13 with 37).
     const int64_t want = std::max(((int64_t)a.max_new + THREADS * TOK_PER_THREAD - 1) / (THREADS * TOK_PER_THREAD),
                                   ((int64_t)a.batch + 15) / 16);

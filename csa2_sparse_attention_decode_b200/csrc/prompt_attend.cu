@@ -48,12 +48,14 @@
 //     rows of O fit beside S; then the softmax (about 1200 of 4800 cycles a
 //     key tile), during which no latents can be loaded either, for all of
 //     shared memory holds the tile in use.  6000 tokens: 2.65 ms, 890 TFLOP/s,
-//     0.53 of the measured bf16 rate.
+//     0.53 of the measured bf16 rate; 2.76 ms in a loop that lasts.
 //   - windows: the chain S, softmax, second product of one token, under the
-//     power limit; 16384 tokens x 128 keys: 450 us, 4.8 TB/s of q and output,
-//     0.74 of the measured copy rate.
+//     power limit; 16384 tokens x 128 keys: 415 us in short runs, 5.2 TB/s of q
+//     and output, 0.81 of the measured copy rate; 490 to 510 us, 4.4 TB/s,
+//     0.68, in a loop that lasts.
 //   - few rows: memory; one token over 131072 latents 45 us (3.0 TB/s), of
-//     which 8 plan and join; 32 tokens over 353600 latents 90 us (4.0 TB/s).
+//     which 8 plan and join; 32 tokens over 353600 latents 89 us (4.1 TB/s),
+//     94 over inputs that change.
 #include "common.cuh"
 #include "serve.cuh"
 #include "umma.cuh"
@@ -1253,9 +1255,11 @@ cudaError_t launch_prompt_attend(const PromptArgs &p, cudaStream_t st)
     // Sharing evens out few rows or ragged pasts (50 tokens after 4000: 57 us
     // against 88 whole; 32 tokens with pasts of 32 to 16384: 34 against 244),
     // but plans and joins (100 tokens after 1000: 43 against 30); many row
-    // tiles are even enough dealt round robin (800 tokens after 20000: 2.38
-    // ms shared, 2.45 whole).  Sliding: one token 9.5 us either way, 4000
-    // tokens 110 against 120 us.
+    // tiles with like pasts are even enough dealt round robin (800 tokens after
+    // 20000: 2.38 ms shared, 2.45 whole).  With one long past among many short
+    // ones they are not, and past MAX_SPLIT_TILES that costs: 131072 latents in
+    // one of 1000 requests with 500 each take 2.95 ms, in one of 800, shared,
+    // 0.16.  Sliding: one token 9.5 us either way, 4000 tokens 110 against 120.
     const bool sliding = p.window > 0 && p.window <= KT && p.heads % RT == 0;
     if (sliding || few_keys(a.tiles, p.n_k, p.window) || a.tiles > MAX_SPLIT_TILES) {
         const int grid = std::min(a.tiles, CTAS);
